@@ -246,6 +246,59 @@ swl_status switch_layer_forward_variant(int64_t T, int64_t d, int64_t d_ff, int6
                                         const float* b_r, const swl_variant* variant,
                                         void* workspace, size_t workspace_bytes, void* stream);
 
+/* ---- One AdamW step over many tensors (the layer's weights and the caller's own) ----
+ * With t = step[0] + 1, lr' = lr * *lr_scale and g = *grad_scale * grad, per element:
+ *   m = beta1 m + (1 - beta1) g,   v = beta2 v + (1 - beta2) g^2
+ *   w = w (1 - lr' weight_decay)
+ *       - lr' / (1 - beta1^t) * m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
+ * in fp32 (bias corrections in fp64), each operation rounded on its own.  w is the
+ * parameter, or its fp32 master copy when there is one (bf16 parameters only): the
+ * parameter is then written, rounded from w, and not read.
+ * States: state_bits = 32: m and v are fp32 [n].  state_bits = 8: m and v are [n]
+ * bytes and m_scale, v_scale are fp32 [ceil(n / SWL_ADAMW_BLOCK)], one per block
+ * of SWL_ADAMW_BLOCK consecutive elements: m = e4m3(m[i]) * m_scale, sqrt(v) =
+ * e4m3(v[i]) * v_scale, each scale the block's largest magnitude over 448.  m is
+ * rounded to nearest; sqrt(v) is rounded stochastically to e4m3's three mantissa
+ * bits with bits drawn from (element, t, seed), so the same call gives the same
+ * result; a non-zero sqrt(v) keeps at least the smallest code, and a block whose
+ * largest magnitude is under 2^-100 is held as zeros.  All-zero bytes and scales
+ * are the zero state.  The step itself uses the unrounded m and v.
+ * A gradient that is not finite makes its element's states and weight not finite
+ * (8-bit states: the states of its whole block).
+ *   tensors, count  host array; tensors of different types may be mixed; n = 0 is
+ *                   allowed (pointers may then be NULL)
+ *   step            DEVICE int32 [2]: the steps made so far, and a word that is
+ *                   zero between calls; step[0] is incremented on the stream, so a
+ *                   captured call counts its replays.  Two calls that share it
+ *                   must not overlap on the GPU.
+ *   grad_scale, lr_scale  device fp32 [1] or NULL for 1 (gradient clipping or loss
+ *                   scaling; a schedule under graph replay)
+ * param, grad, m, v, master: 16-byte aligned, step 8-byte (SWL_ERR_UNSUPPORTED).
+ * What the step writes must overlap neither itself (the same tensor twice) nor a
+ * gradient or scale: SWL_ERR_INVALID_ARG, as are lr < 0, beta outside [0, 1),
+ * eps <= 0 or a negative weight_decay.  No workspace: up to 160 tensors go in one launch. */
+#define SWL_ADAMW_BLOCK 256
+typedef struct swl_adamw_tensor {
+  int64_t n;            /* elements */
+  int dtype;            /* SWL_F32 or SWL_BF16: dtype of param and grad */
+  int state_bits;       /* 32 or 8 */
+  double weight_decay;
+  void* param;
+  const void* grad;
+  void* m;
+  void* v;
+  float* m_scale;       /* state_bits = 8 only, else NULL */
+  float* v_scale;
+  float* master;        /* fp32 [n] or NULL (bf16 parameters only) */
+} swl_adamw_tensor;
+typedef struct swl_adamw {
+  double lr, beta1, beta2, eps;
+  uint32_t seed;        /* of the 8-bit states' rounding */
+} swl_adamw;
+swl_status switch_layer_adamw_step(const swl_adamw_tensor* tensors, int count,
+                                   const swl_adamw* cfg, int32_t* step, const float* grad_scale,
+                                   const float* lr_scale, void* stream);
+
 /* As switch_layer_forward, and records cudaEvent_t stage_events[k] on `stream`
  * before stage 0 (k = 0) and after stage k-1 (k = 1..SWL_NUM_STAGES): an array
  * of SWL_NUM_STAGES + 1 events created by the caller (timing enabled). */

@@ -12,6 +12,7 @@ allocates the outputs and the workspace with torch and calls
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional, Sequence
@@ -46,7 +47,8 @@ EXPORTS = ("switch_layer_capacity", "switch_layer_workspace_size", "switch_layer
            "switch_layer_ep_workspace_size", "switch_layer_ep_counts",
            "switch_layer_ep_dispatch", "switch_layer_ep_experts", "switch_layer_ep_combine",
            "switch_layer_variant_workspace_size", "switch_layer_forward_variant",
-           "switch_layer_backward_workspace_size", "switch_layer_backward")
+           "switch_layer_backward_workspace_size", "switch_layer_backward",
+           "switch_layer_adamw_step")
 SWL_ACT_RELU, SWL_ACT_GEGLU = 0, 1
 
 
@@ -54,6 +56,24 @@ class Variant(ctypes.Structure):
     """struct swl_variant of include/switch_layer.h."""
     _fields_ = [("top_k", ctypes.c_int), ("normalize", ctypes.c_int),
                 ("activation", ctypes.c_int), ("router_noise", ctypes.c_void_p)]
+
+
+class AdamwTensor(ctypes.Structure):
+    """struct swl_adamw_tensor of include/switch_layer.h."""
+    _fields_ = [("n", ctypes.c_int64), ("dtype", ctypes.c_int), ("state_bits", ctypes.c_int),
+                ("weight_decay", ctypes.c_double), ("param", ctypes.c_void_p),
+                ("grad", ctypes.c_void_p), ("m", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("m_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+                ("master", ctypes.c_void_p)]
+
+
+class Adamw(ctypes.Structure):
+    """struct swl_adamw of include/switch_layer.h."""
+    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
+                ("eps", ctypes.c_double), ("seed", ctypes.c_uint32)]
+
+
+SWL_ADAMW_BLOCK = 256
 SWL_ROUTER_TENSOR = 0
 SWL_ROUTER_FFMA = 1
 SWL_NOALLOC_MAX_BYTES = 64 << 20
@@ -167,6 +187,9 @@ def lib() -> ctypes.CDLL:
     L.switch_layer_forward_shard_end.argtypes = [_i64, _i64, _i64, _i64, _i32, _i64, _i32,
                                                  _i32, _vp, _vp, _vp, _vp, _vp, _vp, _dbl,
                                                  _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]
+    L.switch_layer_adamw_step.restype = _i32
+    L.switch_layer_adamw_step.argtypes = [ctypes.POINTER(AdamwTensor), _i32,
+                                          ctypes.POINTER(Adamw), _vp, _vp, _vp, _vp]
     _lib = L
     return L
 
@@ -743,3 +766,114 @@ def backward(inputs: dict, capacity_factor: float, fwd: dict, fwd_workspace: tor
     if check:
         _check(switch_layer_device_status(fwd_workspace, stream), "device status")
     return g
+
+
+# ---------------------------------------------------------------------------
+# AdamW
+# ---------------------------------------------------------------------------
+def _one_device(tensors) -> torch.device:
+    """The device that all of these CUDA tensors are on (None entries are skipped)."""
+    dev = None
+    for t in tensors:
+        if t is None:
+            continue
+        if dev is None:
+            dev = t.device
+        elif t.device != dev:
+            raise ValueError("tensors on %s and %s: all must be on one device" % (dev, t.device))
+    return dev
+
+
+def _on(dev: torch.device):
+    """A context in which ``dev`` is the current device (the library launches there)."""
+    if dev.index is None or dev.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(dev)
+
+
+def adamw_state(params: Sequence[torch.Tensor], state_bits: int = 32,
+                master: bool = False) -> dict:
+    """Zero states for ``adamw_step`` over ``params``: lists ``m``, ``v`` (and ``m_scale``,
+    ``v_scale`` with 8-bit states, ``master`` fp32 copies of the bf16 parameters when
+    ``master``), and ``step``, the device counter."""
+    if state_bits not in (8, 32):
+        raise ValueError("state_bits must be 8 or 32, got %r" % (state_bits,))
+    dev = _one_device(params)
+    if dev is None:
+        raise ValueError("adamw_state needs at least one parameter")
+    for p in params:
+        _require(p, "param")
+        dtype_code(p.dtype)
+    eight = state_bits == 8
+    dt = torch.float8_e4m3fn if eight else torch.float32
+
+    def zeros(n, t):
+        return torch.zeros(n, dtype=torch.uint8 if t == torch.float8_e4m3fn else t,
+                           device=dev).view(t)
+
+    nb = [-(-p.numel() // SWL_ADAMW_BLOCK) for p in params]
+    return {"m": [zeros(p.numel(), dt) for p in params],
+            "v": [zeros(p.numel(), dt) for p in params],
+            "m_scale": [zeros(n, torch.float32) if eight else None for n in nb],
+            "v_scale": [zeros(n, torch.float32) if eight else None for n in nb],
+            "master": [p.detach().float() if master and p.dtype == torch.bfloat16 else None
+                       for p in params],
+            "step": torch.zeros(2, dtype=torch.int32, device=dev)}
+
+
+def adamw_step(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], state: dict,
+               lr: float = 1e-3, betas=(0.9, 0.999), eps: float = 1e-8, weight_decay=0.0,
+               grad_scale: Optional[torch.Tensor] = None,
+               lr_scale: Optional[torch.Tensor] = None, seed: int = 0, stream=None) -> None:
+    """One AdamW step over all ``params`` in place (see switch_layer_adamw_step in
+    include/switch_layer.h).  ``state`` is adamw_state's; ``weight_decay`` is one number or
+    one per tensor; ``grad_scale`` and ``lr_scale`` are fp32 device tensors of one element."""
+    n = len(params)
+    wds = weight_decay if isinstance(weight_decay, (list, tuple)) else [weight_decay] * n
+    lists = [state[k] for k in ("m", "v", "m_scale", "v_scale", "master")]
+    if len(grads) != n or len(wds) != n or any(len(x) != n for x in lists):
+        raise ValueError("params, grads, weight_decay and every list of the state must hold "
+                         "%d entries" % n)
+    step = state["step"]
+    _require(step, "step", torch.int32)
+    if step.numel() != 2:
+        raise ValueError("step must hold 2 values")
+    dev = step.device
+    table = (AdamwTensor * max(1, n))()
+
+    def at(t, name, dtype, count):
+        # _require, the size and the device in one pass (this call is made for every tensor)
+        if not isinstance(t, torch.Tensor) or t.dtype != dtype or not t.is_contiguous():
+            _require(t, name, dtype)
+        if t.device != dev:
+            raise ValueError("%s is on %s: all tensors must be on %s" % (name, t.device, dev))
+        if t.numel() != count:
+            raise ValueError("%s must hold %d values, got %d" % (name, count, t.numel()))
+        return t.data_ptr()
+
+    for i, (p, g, m, v, ms, vs, w) in enumerate(zip(params, grads, *lists)):
+        e = table[i]
+        if not isinstance(p, torch.Tensor):
+            raise TypeError("param must be a torch.Tensor")
+        dt, k = p.dtype, p.numel()
+        e.n, e.dtype, e.weight_decay = k, dtype_code(dt), wds[i]
+        e.param = at(p, "param", dt, k)
+        e.grad = at(g, "grad", dt, k)
+        st = torch.float32
+        e.state_bits = 32
+        if ms is not None or vs is not None:
+            st = torch.float8_e4m3fn
+            e.state_bits = 8
+            nb = -(-k // SWL_ADAMW_BLOCK)
+            e.m_scale = at(ms, "m_scale", torch.float32, nb)
+            e.v_scale = at(vs, "v_scale", torch.float32, nb)
+        e.m = at(m, "m", st, k)
+        e.v = at(v, "v", st, k)
+        if w is not None:
+            e.master = at(w, "master", torch.float32, k)
+    gs = None if grad_scale is None else at(grad_scale, "grad_scale", torch.float32, 1)
+    ls = None if lr_scale is None else at(lr_scale, "lr_scale", torch.float32, 1)
+    cfg = Adamw(lr, betas[0], betas[1], eps, int(seed) & 0xFFFFFFFF)
+    with _on(dev):
+        _check(lib().switch_layer_adamw_step(table, n, ctypes.byref(cfg), step.data_ptr(), gs, ls,
+                                             _stream_handle(stream)), "adamw_step")
