@@ -276,7 +276,8 @@ swl_status switch_layer_forward_variant(int64_t T, int64_t d, int64_t d_ff, int6
  * param, grad, m, v, master: 16-byte aligned, step 8-byte (SWL_ERR_UNSUPPORTED).
  * What the step writes must overlap neither itself (the same tensor twice) nor a
  * gradient or scale: SWL_ERR_INVALID_ARG, as are lr < 0, beta outside [0, 1),
- * eps <= 0 or a negative weight_decay.  No workspace: up to 160 tensors go in one launch. */
+ * eps <= 0 or a negative weight_decay.  No workspace: up to 160 tensors of one kind
+ * (type, master, states) go in one launch. */
 #define SWL_ADAMW_BLOCK 256
 typedef struct swl_adamw_tensor {
   int64_t n;            /* elements */

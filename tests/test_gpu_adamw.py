@@ -2,8 +2,9 @@
 
 u = 2^-24 is half a step of fp32.  Each of the kernel's operations is rounded
 once, so (with the constants' own roundings) m is off by at most 6 u of the sizes
-of its two terms, v by at most 8 u of itself, the denominator by 10 u, and the
-weight by the update's share of these plus 3 u of its own size.
+of its two terms, v by at most 8 u of itself, the denominator by 10 u with its root, the quotient by
+16 u with the division, and the weight by the update's share of these plus 3 u of
+its own size.
 """
 from __future__ import annotations
 
@@ -68,7 +69,7 @@ def _check_step(params0, grads, s0, params, s1, wd, gs=1.0, lrs=1.0):
         root = (v / (1 - B2 ** t)).sqrt() + EPS
         rate = lr / (1 - B1 ** t)
         w = w0 * (1 - lr * wd[i]) - rate * m / root
-        ew = rate * (em / root + 12 * U * m.abs() / root) + 3 * U * (w0.abs() + w.abs()) + 1e-38
+        ew = rate * (em / root + 16 * U * m.abs() / root) + 3 * U * (w0.abs() + w.abs()) + 1e-38
         if s0["master"][i] is not None:
             assert ((s1["master"][i].double() - w).abs() <= ew).all(), i
         half = 2.0 ** -8 * w.abs() if p1.dtype == torch.bfloat16 else 0.0
@@ -128,7 +129,7 @@ def test_mixed_types_and_more_tensors_than_one_launch(bits):
     p0, s0 = [p.clone() for p in params], _clone(state)
     before = swl.switch_layer_launch_count()
     swl.adamw_step(params, grads, state, lr=LR, betas=(B1, B2), eps=EPS)
-    assert swl.switch_layer_launch_count() - before == 3
+    assert swl.switch_layer_launch_count() - before == 3    # 222 of one kind, 111 of the other
     _check_step(p0, grads, s0, params, state, [0.0] * len(sizes))
 
 
