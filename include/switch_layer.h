@@ -246,6 +246,68 @@ swl_status switch_layer_forward_variant(int64_t T, int64_t d, int64_t d_ff, int6
                                         const float* b_r, const swl_variant* variant,
                                         void* workspace, size_t workspace_bytes, void* stream);
 
+/* ---- The norms around a block, with its gate, residual scale and residual ----
+ * The layer adds no residual; this does, with the norms on both sides:
+ *   n(v; w, b) = (v - mu) / sqrt(mean((v - mu)^2) + eps) * w + b, with mu = mean(v)
+ *                (SWL_NORM_LAYER; b optional) or mu = 0 and no b (SWL_NORM_RMS)
+ *   u_t = n(y_t; w_post, b_post), or y_t when w_post is NULL
+ *   r_t = x_t + gate_t * (scale . u_t)     gate NULL: 1, scale NULL: 1
+ *   h_t = n(r_t; w_pre, b_pre)             the next block's input
+ * x is the residual stream, y the block's output (for this layer: out, zero rows for
+ * dropped tokens; for experts run with the grouped products: the combined rows, with
+ * gate the router's).  y NULL: only h = n(x); then r is NULL.  h NULL (and w_pre
+ * NULL): no second norm.  Sums and statistics are fp32; r and h are each rounded
+ * once (h is taken from the unrounded r).
+ *   x, y, r, h      [T, d] of dtype; r and h may be x or y themselves (in place), but
+ *                   not overlap them otherwise, nor each other
+ *   gate [T], w_*, b_*, scale [d]   fp32
+ * d <= 16384 (SWL_ERR_UNSUPPORTED).  No alignment beyond the element's is needed (16
+ * bytes and d a multiple of 16 bytes take the widest loads).  No workspace.  A row of
+ * T that has to stay out (padding) is left out by the caller: every row is written. */
+#define SWL_NORM_RMS 0
+#define SWL_NORM_LAYER 1
+typedef struct swl_norm {
+  int kind;
+  float eps;            /* > 0, finite */
+  const float* w_pre;
+  const float* b_pre;
+  const float* w_post;
+  const float* b_post;
+  const float* scale;
+} swl_norm;
+swl_status switch_layer_norm_residual(int64_t T, int64_t d, int dtype, const void* x,
+                                      const void* y, const float* gate, const swl_norm* norm,
+                                      void* r, void* h, void* stream);
+
+/* Backward pass of switch_layer_norm_residual: the gradients of
+ * sum(dr . r) + sum(dh . h).
+ *   dr       [T, d] gradient of r through its other uses, or NULL for zero
+ *   dh       [T, d] gradient of h (with w_pre, else NULL)
+ *   r, y     the forward's r (x when y is NULL; may be NULL without w_pre) and y;
+ *            the statistics are recomputed from them
+ * grads: dx [T, d] (may be dr itself) and, with y, dy [T, d] are always written; the
+ * others may be NULL: dgate [T], dscale, dw_*, db_* [d], fp32, written (not added
+ * to).  Otherwise outputs overlap neither inputs nor each other.  The column sums run
+ * in a fixed order (the same result every time).  workspace:
+ * switch_layer_norm_residual_backward_workspace_size bytes, 256-byte aligned. */
+typedef struct swl_norm_grads {
+  void* dx;
+  void* dy;
+  float* dgate;
+  float* dw_pre;
+  float* db_pre;
+  float* dw_post;
+  float* db_post;
+  float* dscale;
+} swl_norm_grads;
+swl_status switch_layer_norm_residual_backward_workspace_size(int64_t T, int64_t d, int dtype,
+                                                              size_t* bytes);
+swl_status switch_layer_norm_residual_backward(int64_t T, int64_t d, int dtype, const void* dr,
+                                               const void* dh, const void* r, const void* y,
+                                               const float* gate, const swl_norm* norm,
+                                               const swl_norm_grads* grads, void* workspace,
+                                               size_t workspace_bytes, void* stream);
+
 /* ---- One AdamW step over many tensors (the layer's weights and the caller's own) ----
  * With t = step[0] + 1, lr' = lr * *lr_scale and g = *grad_scale * grad, per element:
  *   m = beta1 m + (1 - beta1) g,   v = beta2 v + (1 - beta2) g^2

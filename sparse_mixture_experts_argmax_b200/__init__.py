@@ -48,7 +48,9 @@ EXPORTS = ("switch_layer_capacity", "switch_layer_workspace_size", "switch_layer
            "switch_layer_ep_dispatch", "switch_layer_ep_experts", "switch_layer_ep_combine",
            "switch_layer_variant_workspace_size", "switch_layer_forward_variant",
            "switch_layer_backward_workspace_size", "switch_layer_backward",
-           "switch_layer_adamw_step")
+           "switch_layer_adamw_step", "switch_layer_norm_residual",
+           "switch_layer_norm_residual_backward_workspace_size",
+           "switch_layer_norm_residual_backward")
 SWL_ACT_RELU, SWL_ACT_GEGLU = 0, 1
 
 
@@ -73,6 +75,20 @@ class Adamw(ctypes.Structure):
                 ("eps", ctypes.c_double), ("seed", ctypes.c_uint32)]
 
 
+class Norm(ctypes.Structure):
+    """struct swl_norm of include/switch_layer.h."""
+    _fields_ = [("kind", ctypes.c_int), ("eps", ctypes.c_float), ("w_pre", ctypes.c_void_p),
+                ("b_pre", ctypes.c_void_p), ("w_post", ctypes.c_void_p),
+                ("b_post", ctypes.c_void_p), ("scale", ctypes.c_void_p)]
+
+
+class NormGrads(ctypes.Structure):
+    """struct swl_norm_grads of include/switch_layer.h."""
+    _fields_ = [(k, ctypes.c_void_p) for k in ("dx", "dy", "dgate", "dw_pre", "db_pre",
+                                               "dw_post", "db_post", "dscale")]
+
+
+SWL_NORM_RMS, SWL_NORM_LAYER = 0, 1
 SWL_ADAMW_BLOCK = 256
 SWL_ROUTER_TENSOR = 0
 SWL_ROUTER_FFMA = 1
@@ -187,6 +203,16 @@ def lib() -> ctypes.CDLL:
     L.switch_layer_forward_shard_end.argtypes = [_i64, _i64, _i64, _i64, _i32, _i64, _i32,
                                                  _i32, _vp, _vp, _vp, _vp, _vp, _vp, _dbl,
                                                  _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]
+    L.switch_layer_norm_residual.restype = _i32
+    L.switch_layer_norm_residual.argtypes = [_i64, _i64, _i32, _vp, _vp, _vp,
+                                             ctypes.POINTER(Norm), _vp, _vp, _vp]
+    L.switch_layer_norm_residual_backward_workspace_size.restype = _i32
+    L.switch_layer_norm_residual_backward_workspace_size.argtypes = [_i64, _i64, _i32,
+                                                                     ctypes.POINTER(_sz)]
+    L.switch_layer_norm_residual_backward.restype = _i32
+    L.switch_layer_norm_residual_backward.argtypes = [_i64, _i64, _i32, _vp, _vp, _vp, _vp, _vp,
+                                                      ctypes.POINTER(Norm),
+                                                      ctypes.POINTER(NormGrads), _vp, _sz, _vp]
     L.switch_layer_adamw_step.restype = _i32
     L.switch_layer_adamw_step.argtypes = [ctypes.POINTER(AdamwTensor), _i32,
                                           ctypes.POINTER(Adamw), _vp, _vp, _vp, _vp]
@@ -769,6 +795,127 @@ def backward(inputs: dict, capacity_factor: float, fwd: dict, fwd_workspace: tor
 
 
 # ---------------------------------------------------------------------------
+# the operators around the layer: shared checks
+# ---------------------------------------------------------------------------
+def _at(t: Optional[torch.Tensor], name: str, dtype, shape, dev) -> Optional[int]:
+    """The address of a contiguous CUDA tensor of this type, shape and device (None: None)."""
+    if t is None:
+        return None
+    if (not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != dtype or
+            not t.is_contiguous()):
+        _require(t, name, dtype)
+    if t.device != dev:
+        raise ValueError("%s is on %s: all tensors must be on %s" % (name, t.device, dev))
+    if t.shape != shape:
+        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+    return t.data_ptr()
+
+
+def _on(dev: torch.device):
+    """A context in which ``dev`` is the current device (the library launches there)."""
+    if dev.index is None or dev.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(dev)
+
+
+def _allocating_on(stream, dev: torch.device):
+    """A context in which torch allocates for ``stream`` (None: the current one), so that
+    memory freed after the call is not handed out before the stream is done with it."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=dev)
+    return torch.cuda.stream(stream)
+
+
+# ---------------------------------------------------------------------------
+# the norms around a block
+# ---------------------------------------------------------------------------
+_NORM_KINDS = {"rms": SWL_NORM_RMS, "layer": SWL_NORM_LAYER}
+
+
+def _norm_struct(d, dev, kind, eps, w_pre, b_pre, w_post, b_post, scale) -> Norm:
+    if kind not in _NORM_KINDS:
+        raise ValueError("kind must be 'rms' or 'layer', got %r" % (kind,))
+    f, shape = torch.float32, (d,)
+    return Norm(_NORM_KINDS[kind], eps, _at(w_pre, "w_pre", f, shape, dev),
+                _at(b_pre, "b_pre", f, shape, dev), _at(w_post, "w_post", f, shape, dev),
+                _at(b_post, "b_post", f, shape, dev), _at(scale, "scale", f, shape, dev))
+
+
+def norm_residual(x: torch.Tensor, y: Optional[torch.Tensor] = None,
+                  w_pre: Optional[torch.Tensor] = None, b_pre: Optional[torch.Tensor] = None,
+                  w_post: Optional[torch.Tensor] = None, b_post: Optional[torch.Tensor] = None,
+                  gate: Optional[torch.Tensor] = None, scale: Optional[torch.Tensor] = None,
+                  kind: str = "rms", eps: float = 1e-6, r: Optional[torch.Tensor] = None,
+                  h: Optional[torch.Tensor] = None, stream=None) -> dict:
+    """The norms around a block (see switch_layer_norm_residual in include/switch_layer.h):
+    ``r = x + gate * scale * norm(y; w_post, b_post)`` and ``h = norm(r; w_pre, b_pre)``.
+    Without ``y`` ``r`` is ``x`` itself; without ``w_pre`` ``h`` is None.  ``r`` and ``h`` are
+    allocated unless given (``r=x`` adds in place)."""
+    if x.dim() != 2:
+        raise ValueError("x must be [T, d]")
+    dev, dt, shape = x.device, x.dtype, x.shape
+    T, d = shape
+    n = _norm_struct(d, dev, kind, eps, w_pre, b_pre, w_post, b_post, scale)
+    if y is None and r is not None:
+        raise ValueError("r needs y")
+    if w_pre is None and h is not None:
+        raise ValueError("h needs w_pre")
+    if (r is None and y is not None) or (h is None and w_pre is not None):
+        with _allocating_on(stream, dev):
+            r = torch.empty_like(x) if r is None and y is not None else r
+            h = torch.empty_like(x) if h is None and w_pre is not None else h
+    args = (T, d, dtype_code(dt), _at(x, "x", dt, shape, dev), _at(y, "y", dt, shape, dev),
+            _at(gate, "gate", torch.float32, (T,), dev), ctypes.byref(n),
+            _at(r, "r", dt, shape, dev), _at(h, "h", dt, shape, dev))
+    if T > 0:
+        with _on(dev):
+            _check(lib().switch_layer_norm_residual(*args, _stream_handle(stream)),
+                   "norm_residual")
+    return {"r": x if y is None else r, "h": h}
+
+
+def norm_residual_backward(dr: Optional[torch.Tensor], dh: Optional[torch.Tensor],
+                           r: torch.Tensor, y: Optional[torch.Tensor] = None,
+                           w_pre: Optional[torch.Tensor] = None,
+                           b_pre: Optional[torch.Tensor] = None,
+                           w_post: Optional[torch.Tensor] = None,
+                           b_post: Optional[torch.Tensor] = None,
+                           gate: Optional[torch.Tensor] = None,
+                           scale: Optional[torch.Tensor] = None, kind: str = "rms",
+                           eps: float = 1e-6, stream=None) -> dict:
+    """Gradients of ``sum(dr * r) + sum(dh * h)`` of ``norm_residual`` (its ``r`` and its
+    inputs): dx, dy, dgate, dscale, dw_pre, db_pre, dw_post, db_post; None where the forward
+    call had no such input.  ``dr`` None: zero."""
+    if r.dim() != 2:
+        raise ValueError("r must be [T, d]")
+    dev, dt, shape = r.device, r.dtype, r.shape
+    T, d = shape
+    f = torch.float32
+    n = _norm_struct(d, dev, kind, eps, w_pre, b_pre, w_post, b_post, scale)
+    pr, py = _at(r, "r", dt, shape, dev), _at(y, "y", dt, shape, dev)
+    pdr, pdh = _at(dr, "dr", dt, shape, dev), _at(dh, "dh", dt, shape, dev)
+    pg = _at(gate, "gate", f, (T,), dev)
+    nbytes = _sz(0)
+    _check(lib().switch_layer_norm_residual_backward_workspace_size(T, d, dtype_code(dt),
+                                                                    ctypes.byref(nbytes)),
+           "norm_residual_backward_workspace_size")
+    with _allocating_on(stream, dev):
+        ws = torch.empty(nbytes.value, dtype=torch.uint8, device=dev)
+        g = {"dx": torch.empty_like(r), "dy": None if y is None else torch.empty_like(r)}
+        for k, t in (("dgate", gate), ("dscale", scale), ("dw_pre", w_pre), ("db_pre", b_pre),
+                     ("dw_post", w_post), ("db_post", b_post)):
+            g[k] = None if t is None else torch.empty_like(t)
+    o = NormGrads(*[_ptr(g[k]) for k, _ in NormGrads._fields_])
+    with _on(dev):
+        _check(lib().switch_layer_norm_residual_backward(
+            T, d, dtype_code(dt), pdr, pdh, pr, py, pg, ctypes.byref(n), ctypes.byref(o),
+            ws.data_ptr(), ws.numel(), _stream_handle(stream)), "norm_residual_backward")
+    return g
+
+
+# ---------------------------------------------------------------------------
 # AdamW
 # ---------------------------------------------------------------------------
 def _one_device(tensors) -> torch.device:
@@ -782,13 +929,6 @@ def _one_device(tensors) -> torch.device:
         elif t.device != dev:
             raise ValueError("tensors on %s and %s: all must be on one device" % (dev, t.device))
     return dev
-
-
-def _on(dev: torch.device):
-    """A context in which ``dev`` is the current device (the library launches there)."""
-    if dev.index is None or dev.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(dev)
 
 
 def adamw_state(params: Sequence[torch.Tensor], state_bits: int = 32,

@@ -1,0 +1,751 @@
+// The norms before and after a block, fused with the block's gate, the residual
+// scale and the residual addition, and their backward pass.
+//
+//   n(v; w, b) = (v - mu) rho w + b,  rho = 1 / sqrt(mean((v - mu)^2) + eps),
+//                mu = mean(v) (layer norm) or 0 (RMS norm, without b)
+//   u_t = n(y_t; w_post, b_post), or y_t without w_post
+//   r_t = x_t + gate_t * scale . u_t       (r = x without y)
+//   h_t = n(r_t; w_pre, b_pre)             (the next block's input; optional)
+//
+// Backward, from the gradients dr of r (its other uses) and dh of h, with
+// v^ = (v - mu) rho and N(g; v, w) = rho (a - [layer] mean(a) - v^ mean(a v^)),
+// a = w . g:
+//   D = dr + N(dh; r, w_pre),   dx = D,
+//   dgate_t = sum_j D_j scale_j u_j,   dscale = sum_t gate_t D u,
+//   du = gate_t scale . D,   dy = N(du; y, w_post) (du without w_post),
+//   dw_pre = sum_t dh r^, db_pre = sum_t dh, dw_post = sum_t du y^, db_post = sum_t du.
+// The statistics are recomputed from r and y, which the pass reads anyway: the
+// forward pass saves nothing.  h is taken from the unrounded r.
+//
+// Bound: HBM, one read of every input row and one write of every output row
+// (forward 4, backward 6 row-sized arrays).  A row is held in registers by a group
+// of W warps (E elements per thread, 16 bytes per load where widths and pointers
+// allow); sums over the row go through warp shuffles and, for W > 1, one
+// exchange in shared memory behind a barrier of the group alone, so several rows
+// are in flight per SM without waiting for one another.  All sums are fp32, a
+// layer norm's variance is taken about the mean in a second sum.  The parameters'
+// gradients are column sums over all rows: a thread keeps its columns' sums in
+// registers over all the rows it sees (grid-stride), the groups of a CTA add theirs
+// in order, and a second kernel adds the CTAs' sums in order: no atomics, the same
+// result every time.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+
+#include "kernels.h"
+#include "switch_layer.h"
+
+namespace swl {
+namespace {
+
+constexpr int kMaxWarps = 16;         // warps per row, at most
+constexpr int kMaxWidth = 16384;      // 16 warps x 32 lanes x 32 elements
+constexpr int kSums = 5;              // column sums: w_pre, b_pre, w_post, b_post, scale
+
+template <typename T, int V>
+struct Vec;
+template <>
+struct Vec<float, 4> {
+  float4 q;
+  __device__ __forceinline__ void get(float* o) const { o[0] = q.x, o[1] = q.y, o[2] = q.z, o[3] = q.w; }
+  __device__ __forceinline__ void set(const float* o) { q = make_float4(o[0], o[1], o[2], o[3]); }
+};
+template <>
+struct Vec<float, 2> {
+  float2 q;
+  __device__ __forceinline__ void get(float* o) const { o[0] = q.x, o[1] = q.y; }
+};
+template <>
+struct Vec<float, 1> {
+  float q;
+  __device__ __forceinline__ void get(float* o) const { o[0] = q; }
+  __device__ __forceinline__ void set(const float* o) { q = o[0]; }
+};
+__device__ __forceinline__ unsigned pack2(float a, float b) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const unsigned*>(&v);
+}
+template <>
+struct Vec<__nv_bfloat16, 8> {
+  uint4 q;
+  __device__ __forceinline__ void get(float* o) const {
+    const unsigned u[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      o[2 * i] = __uint_as_float(u[i] << 16);
+      o[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+    }
+  }
+  __device__ __forceinline__ void set(const float* o) {
+    q = make_uint4(pack2(o[0], o[1]), pack2(o[2], o[3]), pack2(o[4], o[5]), pack2(o[6], o[7]));
+  }
+};
+template <>
+struct Vec<__nv_bfloat16, 2> {
+  unsigned q;
+  __device__ __forceinline__ void get(float* o) const {
+    o[0] = __uint_as_float(q << 16), o[1] = __uint_as_float(q & 0xffff0000u);
+  }
+  __device__ __forceinline__ void set(const float* o) { q = pack2(o[0], o[1]); }
+};
+template <>
+struct Vec<__nv_bfloat16, 1> {
+  unsigned short q;
+  __device__ __forceinline__ void get(float* o) const { o[0] = __uint_as_float(static_cast<unsigned>(q) << 16); }
+  __device__ __forceinline__ void set(const float* o) {
+    const __nv_bfloat16 v = __float2bfloat16_rn(o[0]);
+    q = *reinterpret_cast<const unsigned short*>(&v);
+  }
+};
+
+struct Params {
+  const float* w_pre;
+  const float* b_pre;
+  const float* w_post;
+  const float* b_post;
+  const float* scale;
+  const float* gate;
+  float eps, inv_d;
+  int d;
+  int64_t T;
+  int W;              // warps per row (a power of two)
+};
+struct FwdArgs {
+  Params p;
+  const void* x;
+  const void* y;
+  void* r;
+  void* h;
+};
+struct BwdArgsN {
+  Params p;
+  const void* dr;
+  const void* dh;
+  const void* r;
+  const void* y;
+  void* dx;
+  void* dy;
+  float* dgate;
+  float* part;        // [grid][kSums][d] column sums of each CTA
+  unsigned wanted;    // bit s: column sum s is asked for
+};
+
+// A thread's place: its group's rows and its own columns (vector k starts at
+// column (k * 32 W + tid) * V).
+template <int V, int E>
+struct Lane {
+  int tid, group, groups, span;     // span: threads of a group
+  __device__ __forceinline__ explicit Lane(int W) {
+    span = 32 * W;
+    group = threadIdx.x / span;
+    tid = threadIdx.x - group * span;
+    groups = blockDim.x / span;
+  }
+  __device__ __forceinline__ int col(int k) const { return (k * span + tid) * V; }
+};
+
+template <typename T, int V, int E>
+struct Row {
+  Vec<T, V> v[E / V];
+  __device__ __forceinline__ void load(const void* base, int64_t row, int d, const Lane<V, E>& l) {
+    const T* p = static_cast<const T*>(base) + row * d;
+#pragma unroll
+    for (int k = 0; k < E / V; ++k) {
+      const int c = l.col(k);
+      if (c < d) v[k].q = *reinterpret_cast<const decltype(v[k].q)*>(p + c);
+      else v[k].q = decltype(v[k].q){};
+    }
+  }
+  __device__ __forceinline__ void get(float (&o)[E]) const {
+#pragma unroll
+    for (int k = 0; k < E / V; ++k) v[k].get(o + k * V);
+  }
+};
+template <typename T, int V, int E>
+__device__ __forceinline__ void store_row(void* base, int64_t row, int d, const Lane<V, E>& l,
+                                          const float (&o)[E]) {
+  T* p = static_cast<T*>(base) + row * d;
+#pragma unroll
+  for (int k = 0; k < E / V; ++k) {
+    const int c = l.col(k);
+    Vec<T, V> v;
+    v.set(o + k * V);
+    if (c < d) *reinterpret_cast<decltype(v.q)*>(p + c) = v.q;
+  }
+}
+// A parameter vector's values at this thread's columns (fp32; the loads hit L1).
+template <int V, int E>
+__device__ __forceinline__ void load_param(const float* p, int d, const Lane<V, E>& l,
+                                           float (&o)[E]) {
+  constexpr int F = V > 4 ? 4 : V;      // floats per load
+#pragma unroll
+  for (int k = 0; k < E / V; ++k) {
+    const int c = l.col(k);
+#pragma unroll
+    for (int i = 0; i < V; i += F) {
+      Vec<float, F> v;
+      if (c < d) {
+        v.q = __ldg(reinterpret_cast<const decltype(v.q)*>(p + c + i));
+        v.get(o + k * V + i);
+      } else {
+#pragma unroll
+        for (int j = 0; j < F; ++j) o[k * V + i + j] = 0.f;
+      }
+    }
+  }
+}
+
+// Sums over the row of N values per thread, the same in every thread.  The two
+// buffers alternate, so one barrier per sum is enough: a thread that writes a
+// buffer again has passed the next sum's barrier, which follows every read.
+template <int N>
+__device__ __forceinline__ void row_sum(float (&v)[N], int W, float (*buf)[kMaxWarps][4],
+                                        int& turn) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+  if (W == 1) return;
+  const int warp = threadIdx.x >> 5, group = warp / W;
+  float(*b)[4] = buf[turn];
+  turn ^= 1;
+  if ((threadIdx.x & 31) == 0)
+#pragma unroll
+    for (int i = 0; i < N; ++i) b[warp][i] = v[i];
+  asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(32 * W) : "memory");
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = 0.f;
+  for (int w = 0; w < W; ++w)
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] += b[group * W + w][i];
+}
+
+// v becomes v - mu (layer norm; v itself for RMS norm); returns rho.
+template <bool kLayer, int V, int E>
+__device__ __forceinline__ float center(float (&v)[E], const Params& p, const Lane<V, E>& l,
+                                        float (*buf)[kMaxWarps][4], int& turn) {
+  if constexpr (kLayer) {
+    float s[1] = {0.f};
+#pragma unroll
+    for (int i = 0; i < E; ++i) s[0] += v[i];       // columns past d hold zeros
+    row_sum(s, p.W, buf, turn);
+    const float mu = s[0] * p.inv_d;
+#pragma unroll
+    for (int i = 0; i < E; ++i) v[i] = l.col(i / V) < p.d ? v[i] - mu : 0.f;
+  }
+  float s[1] = {0.f};
+#pragma unroll
+  for (int i = 0; i < E; ++i) s[0] = fmaf(v[i], v[i], s[0]);
+  row_sum(s, p.W, buf, turn);
+  return 1.f / sqrtf(s[0] * p.inv_d + p.eps);
+}
+
+template <typename T, int V, int E, bool kLayer>
+__global__ void __launch_bounds__(512, 1)
+norm_residual_kernel(const __grid_constant__ FwdArgs a) {
+  __shared__ float buf[2][kMaxWarps][4];
+  const Params& p = a.p;
+  const Lane<V, E> l(p.W);
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * l.groups;
+  int64_t row = static_cast<int64_t>(blockIdx.x) * l.groups + l.group;
+  int turn = 0;
+  Row<T, V, E> qx, qy;
+  float gate = 1.f;
+  auto fetch = [&](int64_t t) {
+    qx.load(a.x, t, p.d, l);
+    if (a.y) qy.load(a.y, t, p.d, l);
+    if (p.gate) gate = p.gate[t];
+  };
+  if (row < p.T) fetch(row);
+  for (; row < p.T; row += stride) {
+    float r[E], w[E];
+    qx.get(r);
+    float u[E];
+    const float g = gate;
+    if (a.y) qy.get(u);
+    if (row + stride < p.T) fetch(row + stride);     // the next row, under this row's sums
+    if (a.y) {
+      if (p.w_post) {
+        const float rho = center<kLayer>(u, p, l, buf, turn);
+        load_param(p.w_post, p.d, l, w);
+#pragma unroll
+        for (int i = 0; i < E; ++i) u[i] = u[i] * rho * w[i];
+        if (kLayer && p.b_post) {
+          load_param(p.b_post, p.d, l, w);
+#pragma unroll
+          for (int i = 0; i < E; ++i) u[i] += w[i];
+        }
+      }
+      if (p.scale) {
+        load_param(p.scale, p.d, l, w);
+#pragma unroll
+        for (int i = 0; i < E; ++i) u[i] *= w[i];
+      }
+#pragma unroll
+      for (int i = 0; i < E; ++i) r[i] = fmaf(g, u[i], r[i]);
+      store_row<T>(a.r, row, p.d, l, r);
+    }
+    if (a.h) {
+      const float rho = center<kLayer>(r, p, l, buf, turn);
+      load_param(p.w_pre, p.d, l, w);
+#pragma unroll
+      for (int i = 0; i < E; ++i) r[i] = r[i] * rho * w[i];
+      if (kLayer && p.b_pre) {
+        load_param(p.b_pre, p.d, l, w);
+#pragma unroll
+        for (int i = 0; i < E; ++i) r[i] += w[i];
+      }
+      store_row<T>(a.h, row, p.d, l, r);
+    }
+  }
+}
+
+// Row statistics of the backward pass: v becomes v - mu; returns rho, and
+// (through m0, m1) mean(a) and mean(a (v - mu)).
+template <bool kLayer, int V, int E>
+__device__ __forceinline__ float center_with(float (&v)[E], const float (&a)[E], const Params& p,
+                                             const Lane<V, E>& l, float (*buf)[kMaxWarps][4],
+                                             int& turn, float& m0, float& m1) {
+  m0 = 0.f;
+  if constexpr (kLayer) {
+    float s[2] = {0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      s[0] += v[i];
+      s[1] += a[i];
+    }
+    row_sum(s, p.W, buf, turn);
+    const float mu = s[0] * p.inv_d;
+    m0 = s[1] * p.inv_d;
+#pragma unroll
+    for (int i = 0; i < E; ++i) v[i] = l.col(i / V) < p.d ? v[i] - mu : 0.f;
+  }
+  float s[2] = {0.f, 0.f};
+#pragma unroll
+  for (int i = 0; i < E; ++i) {
+    s[0] = fmaf(v[i], v[i], s[0]);
+    s[1] = fmaf(a[i], v[i], s[1]);
+  }
+  row_sum(s, p.W, buf, turn);
+  m1 = s[1] * p.inv_d;
+  return 1.f / sqrtf(s[0] * p.inv_d + p.eps);
+}
+
+template <typename T, int V, int E, bool kLayer>
+__global__ void __launch_bounds__(512, 1)
+norm_residual_bwd_kernel(const __grid_constant__ BwdArgsN a) {
+  extern __shared__ float columns[];        // [d], when a CTA has several groups
+  __shared__ float buf[2][kMaxWarps][4];
+  const Params& p = a.p;
+  const Lane<V, E> l(p.W);
+  pdl_trigger();
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * l.groups;
+  int64_t row = static_cast<int64_t>(blockIdx.x) * l.groups + l.group;
+  int turn = 0;
+  float acc[kSums][E];      // (RMS norm: the two bias sums are never touched)
+#pragma unroll
+  for (int s = 0; s < kSums; ++s)
+#pragma unroll
+    for (int i = 0; i < E; ++i) acc[s][i] = 0.f;
+  Row<T, V, E> qr, qh, qv, qy;
+  auto fetch = [&](int64_t t) {
+    if (a.dr) qr.load(a.dr, t, p.d, l);
+    if (a.dh) {
+      qh.load(a.dh, t, p.d, l);
+      qv.load(a.r, t, p.d, l);
+    }
+    if (a.y) qy.load(a.y, t, p.d, l);
+  };
+  if (row < p.T) fetch(row);
+  for (; row < p.T; row += stride) {
+    float D[E], w[E];
+    if (a.dr) {
+      qr.get(D);
+    } else {
+#pragma unroll
+      for (int i = 0; i < E; ++i) D[i] = 0.f;
+    }
+    float g[E], v[E], y[E];
+    if (a.dh) {
+      qh.get(g);
+      qv.get(v);
+    }
+    if (a.y) qy.get(y);
+    if (row + stride < p.T) fetch(row + stride);
+    if (a.dh) {
+      load_param(p.w_pre, p.d, l, w);
+      if constexpr (kLayer) {
+#pragma unroll
+        for (int i = 0; i < E; ++i) acc[1][i] += g[i];
+      }
+      float b[E];
+#pragma unroll
+      for (int i = 0; i < E; ++i) b[i] = g[i] * w[i];
+      float m0, m1;
+      const float rho = center_with<kLayer>(v, b, p, l, buf, turn, m0, m1);
+      const float m2 = m1 * rho * rho;
+#pragma unroll
+      for (int i = 0; i < E; ++i) {
+        acc[0][i] = fmaf(g[i], v[i] * rho, acc[0][i]);
+        const float t = (kLayer ? b[i] - m0 : b[i]) - v[i] * m2;
+        D[i] = fmaf(t, rho, D[i]);
+      }
+    }
+    store_row<T>(a.dx, row, p.d, l, D);
+    if (!a.y) continue;
+    const float gate = p.gate ? p.gate[row] : 1.f;
+    // D becomes scale . D (no gate): the gate's gradient needs it without the gate
+    float sD[E];
+    if (p.scale) {
+      load_param(p.scale, p.d, l, w);
+#pragma unroll
+      for (int i = 0; i < E; ++i) sD[i] = D[i] * w[i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < E; ++i) sD[i] = D[i];
+    }
+    if (p.w_post) {
+      const float rho = center<kLayer>(y, p, l, buf, turn);
+      load_param(p.w_post, p.d, l, w);
+      float bias[E];
+      if (kLayer && p.b_post) {
+        load_param(p.b_post, p.d, l, bias);
+      } else {
+#pragma unroll
+        for (int i = 0; i < E; ++i) bias[i] = 0.f;
+      }
+      float s[3] = {0.f, 0.f, 0.f};       // sD w, sD w y^, sD b
+#pragma unroll
+      for (int i = 0; i < E; ++i) {
+        const float hat = y[i] * rho;
+        acc[4][i] = fmaf(gate * D[i], kLayer ? fmaf(hat, w[i], bias[i]) : hat * w[i], acc[4][i]);
+        acc[2][i] = fmaf(gate * sD[i], hat, acc[2][i]);
+        if constexpr (kLayer) {
+          acc[3][i] = fmaf(gate, sD[i], acc[3][i]);
+          s[2] = fmaf(sD[i], bias[i], s[2]);
+        }
+        sD[i] *= w[i];
+        if constexpr (kLayer) s[0] += sD[i];
+        s[1] = fmaf(sD[i], hat, s[1]);
+        y[i] = hat;
+      }
+      if constexpr (kLayer) {
+        row_sum(s, p.W, buf, turn);
+      } else {
+        float one[1] = {s[1]};
+        row_sum(one, p.W, buf, turn);
+        s[1] = one[0];
+      }
+      if (a.dgate && l.tid == 0) a.dgate[row] = s[1] + s[2];
+      const float m0 = s[0] * p.inv_d, m1 = s[1] * p.inv_d, f = gate * rho;
+#pragma unroll
+      for (int i = 0; i < E; ++i) sD[i] = ((kLayer ? sD[i] - m0 : sD[i]) - y[i] * m1) * f;
+    } else {
+      float s[1] = {0.f};
+#pragma unroll
+      for (int i = 0; i < E; ++i) {
+        acc[4][i] = fmaf(gate * D[i], y[i], acc[4][i]);
+        s[0] = fmaf(sD[i], y[i], s[0]);
+        sD[i] *= gate;
+      }
+      if (a.dgate) {
+        row_sum(s, p.W, buf, turn);
+        if (l.tid == 0) a.dgate[row] = s[0];
+      }
+    }
+    store_row<T>(a.dy, row, p.d, l, sD);
+  }
+  // this CTA's column sums: its groups add theirs in order
+  float* part = a.part + static_cast<size_t>(blockIdx.x) * kSums * p.d;
+#pragma unroll
+  for (int s = 0; s < kSums; ++s) {
+    if (!(a.wanted >> s & 1u)) continue;
+    for (int g = 0; g < l.groups; ++g) {
+      if (l.groups > 1) __syncthreads();
+      if (l.group != g) continue;
+#pragma unroll
+      for (int i = 0; i < E; ++i) {
+        const int c = l.col(i / V) + i % V;
+        if (c >= p.d) continue;
+        const float v = g == 0 ? acc[s][i] : acc[s][i] + columns[c];
+        if (g == l.groups - 1) part[static_cast<size_t>(s) * p.d + c] = v;
+        else columns[c] = v;
+      }
+    }
+  }
+}
+
+struct SumArgs {
+  const float* part;
+  float* out[kSums];
+  int parts, d;
+};
+// out[s][c] = sum over the CTAs' partial sums, in a fixed order: 16 interleaved
+// runs of CTAs per column, then the runs.
+__global__ void __launch_bounds__(512)
+norm_residual_sum_kernel(const __grid_constant__ SumArgs a) {
+  __shared__ float buf[16][33];
+  const int c = blockIdx.x * 32 + (threadIdx.x & 31), k = threadIdx.x >> 5, s = blockIdx.y;
+  pdl_wait();
+  if (!a.out[s]) return;
+  float v = 0.f;
+  if (c < a.d) {
+    const float* p = a.part + static_cast<size_t>(s) * a.d + c;
+#pragma unroll 4
+    for (int i = k; i < a.parts; i += 16) v += p[static_cast<size_t>(i) * kSums * a.d];
+  }
+  buf[k][threadIdx.x & 31] = v;
+  __syncthreads();
+  if (k == 0 && c < a.d) {
+    v = 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v += buf[i][threadIdx.x & 31];
+    a.out[s][c] = v;
+  }
+}
+
+// ---------------------------------------------------------------- host
+struct Plan {
+  int V, E, W, threads, groups;
+};
+bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+// Rows of up to 4096 elements: 8 elements per thread; wider rows 16 or 32, since
+// a row has 16 warps at most.  `elems`: pointers into rows; `params`: fp32 vectors.
+Plan make_plan(int64_t d, int dtype, std::initializer_list<const void*> elems,
+               std::initializer_list<const float*> params) {
+  Plan q;
+  const int full = dtype == SWL_BF16 ? 8 : 4;
+  auto fits = [&](int v) {
+    if (d % v) return false;
+    for (const void* e : elems)
+      if (!aligned(e, dtype == SWL_BF16 ? 2 * v : 4 * v)) return false;
+    for (const float* f : params)
+      if (!aligned(f, v > 4 ? 16 : 4 * v)) return false;
+    return true;
+  };
+  q.V = fits(full) ? full : dtype == SWL_BF16 && fits(2) ? 2 : 1;
+  q.E = d <= 4096 ? 8 : d <= 8192 ? 16 : 32;
+  q.W = 1;
+  while (q.W * 32 * q.E < d) q.W *= 2;
+  q.threads = q.W <= 8 ? 256 : 32 * q.W;
+  q.groups = q.threads / (32 * q.W);
+  return q;
+}
+
+template <typename F>
+bool dispatch(const Plan& q, int dtype, bool layer, F f) {
+#define SWL_E(T, V, L)                                        \
+  switch (q.E) {                                              \
+    case 8: return f.template run<T, V, 8, L>();              \
+    case 16: return f.template run<T, V, 16, L>();            \
+    default: return f.template run<T, V, 32, L>();            \
+  }
+#define SWL_L(T, V)                  \
+  if (layer) {                       \
+    SWL_E(T, V, true)                \
+  } else {                           \
+    SWL_E(T, V, false)               \
+  }
+  if (dtype == SWL_BF16) {
+    if (q.V == 8) { SWL_L(__nv_bfloat16, 8) }
+    if (q.V == 2) { SWL_L(__nv_bfloat16, 2) }
+    SWL_L(__nv_bfloat16, 1)
+  }
+  if (q.V == 4) { SWL_L(float, 4) }
+  SWL_L(float, 1)
+#undef SWL_L
+#undef SWL_E
+}
+
+struct RunFwd {
+  const FwdArgs& a;
+  const Plan& q;
+  int grid;
+  cudaStream_t st;
+  template <typename T, int V, int E, bool L>
+  bool run() {
+    norm_residual_kernel<T, V, E, L><<<grid, q.threads, 0, st>>>(a);
+    return cudaGetLastError() == cudaSuccess;
+  }
+};
+struct RunBwd {
+  const BwdArgsN& a;
+  const Plan& q;
+  int grid;
+  cudaStream_t st;
+  template <typename T, int V, int E, bool L>
+  bool run() {
+    const size_t smem = q.groups > 1 ? static_cast<size_t>(a.p.d) * 4 : 0;
+    norm_residual_bwd_kernel<T, V, E, L><<<grid, q.threads, smem, st>>>(a);
+    return cudaGetLastError() == cudaSuccess;
+  }
+};
+
+int sm_count() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+  return n;
+}
+
+constexpr int kBwdCtasPerSm = 2;
+constexpr int kMaxSms = 256;     // the workspace is sized without asking the device
+
+swl_status check(int64_t T, int64_t d, int dtype, const swl_norm* n, bool y, bool pre) {
+  if (T < 0 || d <= 0 || (dtype != SWL_F32 && dtype != SWL_BF16) || !n) return SWL_ERR_INVALID_ARG;
+  if (n->kind != SWL_NORM_RMS && n->kind != SWL_NORM_LAYER) return SWL_ERR_INVALID_ARG;
+  if (!std::isfinite(n->eps) || !(n->eps > 0)) return SWL_ERR_INVALID_ARG;
+  if (n->kind == SWL_NORM_RMS && (n->b_pre || n->b_post)) return SWL_ERR_INVALID_ARG;
+  if ((n->b_pre && !n->w_pre) || (n->b_post && !n->w_post)) return SWL_ERR_INVALID_ARG;
+  if (!y && (n->w_post || n->scale)) return SWL_ERR_INVALID_ARG;
+  if (!y && !pre) return SWL_ERR_INVALID_ARG;
+  if (pre != (n->w_pre != nullptr)) return SWL_ERR_INVALID_ARG;
+  if (d > kMaxWidth || T > (int64_t{1} << 40)) return SWL_ERR_UNSUPPORTED;
+  for (const float* f : {n->w_pre, n->b_pre, n->w_post, n->b_post, n->scale})
+    if (!aligned(f, 4)) return SWL_ERR_UNSUPPORTED;
+  return SWL_OK;
+}
+
+Params params_of(int64_t T, int64_t d, const swl_norm* n, const float* gate, int W) {
+  return {n->w_pre, n->b_pre, n->w_post, n->b_post, n->scale, gate, n->eps,
+          static_cast<float>(1.0 / static_cast<double>(d)), static_cast<int>(d), T, W};
+}
+
+// Do [a, a + na) and [b, b + nb) share a byte?  (NULL: no)
+bool meet(const void* a, size_t na, const void* b, size_t nb) {
+  if (!a || !b || !na || !nb) return false;
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + nb && y < x + na;
+}
+
+}  // namespace
+}  // namespace swl
+
+using namespace swl;
+
+extern "C" swl_status switch_layer_norm_residual(int64_t T, int64_t d, int dtype, const void* x,
+                                                 const void* y, const float* gate,
+                                                 const swl_norm* norm, void* r, void* h,
+                                                 void* stream) {
+  swl_status st = check(T, d, dtype, norm, y != nullptr || T == 0, h != nullptr || (T == 0 && norm && norm->w_pre));
+  if (st != SWL_OK) return st;
+  if (T == 0) return SWL_OK;
+  if (!x || (y != nullptr) != (r != nullptr) || (gate && !y)) return SWL_ERR_INVALID_ARG;
+  const uintptr_t e = dtype == SWL_BF16 ? 2 : 4;
+  for (const void* p : {x, y, static_cast<const void*>(r), static_cast<const void*>(h)})
+    if (!aligned(p, e)) return SWL_ERR_UNSUPPORTED;
+  if (!aligned(gate, 4)) return SWL_ERR_UNSUPPORTED;
+  // r and h may be x or y themselves (a thread has read its columns before it
+  // writes them), but not lie across them, nor on a parameter
+  const size_t n = static_cast<size_t>(T) * d * e, nd = static_cast<size_t>(d) * 4;
+  if (meet(r, n, h, n)) return SWL_ERR_INVALID_ARG;
+  for (const void* o : {static_cast<const void*>(r), static_cast<const void*>(h)}) {
+    for (const void* i : {x, y})
+      if (o != i && meet(o, n, i, n)) return SWL_ERR_INVALID_ARG;
+    if (meet(o, n, gate, static_cast<size_t>(T) * 4)) return SWL_ERR_INVALID_ARG;
+    for (const float* f : {norm->w_pre, norm->b_pre, norm->w_post, norm->b_post, norm->scale})
+      if (meet(o, n, f, nd)) return SWL_ERR_INVALID_ARG;
+  }
+  const int sms = sm_count();
+  if (sms <= 0) return SWL_ERR_CUDA;
+  const Plan q = make_plan(d, dtype, {x, y, r, h},
+                           {norm->w_pre, norm->b_pre, norm->w_post, norm->b_post, norm->scale});
+  const FwdArgs a = {params_of(T, d, norm, gate, q.W), x, y, r, h};
+  const int64_t want = (T + q.groups - 1) / q.groups;
+  const int64_t most = static_cast<int64_t>(sms) * (q.threads <= 256 ? 4 : 2);
+  RunFwd run = {a, q, static_cast<int>(want < most ? want : most), static_cast<cudaStream_t>(stream)};
+  if (!dispatch(q, dtype, norm->kind == SWL_NORM_LAYER, run)) return SWL_ERR_CUDA;
+  count_launch();
+  return SWL_OK;
+}
+
+extern "C" swl_status switch_layer_norm_residual_backward_workspace_size(int64_t T, int64_t d,
+                                                                         int dtype,
+                                                                         size_t* bytes) {
+  if (T < 0 || d <= 0 || (dtype != SWL_F32 && dtype != SWL_BF16) || !bytes)
+    return SWL_ERR_INVALID_ARG;
+  if (d > kMaxWidth || T > (int64_t{1} << 40)) return SWL_ERR_UNSUPPORTED;
+  const int64_t most = static_cast<int64_t>(kMaxSms) * kBwdCtasPerSm;
+  *bytes = static_cast<size_t>(T < most ? (T > 0 ? T : 1) : most) * kSums * d * 4;
+  return SWL_OK;
+}
+
+extern "C" swl_status switch_layer_norm_residual_backward(
+    int64_t T, int64_t d, int dtype, const void* dr, const void* dh, const void* r, const void* y,
+    const float* gate, const swl_norm* norm, const swl_norm_grads* grads, void* workspace,
+    size_t workspace_bytes, void* stream) {
+  const bool pre = norm && norm->w_pre;
+  swl_status st = check(T, d, dtype, norm, y != nullptr || T == 0, pre);
+  if (st != SWL_OK) return st;
+  if (!grads || !workspace) return SWL_ERR_INVALID_ARG;
+  const swl_norm_grads& o = *grads;
+  if (T > 0) {
+    if ((dh != nullptr) != pre || (pre && !r) || (!dr && !dh) || !o.dx ||
+        (y != nullptr) != (o.dy != nullptr) || (gate && !y) || (o.dgate && !gate))
+      return SWL_ERR_INVALID_ARG;
+  }
+  if ((o.dw_pre && !norm->w_pre) || (o.db_pre && !norm->b_pre) || (o.dw_post && !norm->w_post) ||
+      (o.db_post && !norm->b_post) || (o.dscale && !norm->scale))
+    return SWL_ERR_INVALID_ARG;
+  const uintptr_t e = dtype == SWL_BF16 ? 2 : 4;
+  const void* in[4] = {dr, dh, r, y};
+  for (const void* p : in)
+    if (!aligned(p, e)) return SWL_ERR_UNSUPPORTED;
+  float* const sums[kSums] = {o.dw_pre, o.db_pre, o.dw_post, o.db_post, o.dscale};
+  for (const float* p : sums)
+    if (!aligned(p, 4)) return SWL_ERR_UNSUPPORTED;
+  if (!aligned(o.dx, e) || !aligned(o.dy, e) || !aligned(o.dgate, 4) || !aligned(gate, 4) ||
+      !aligned(workspace, 256))
+    return SWL_ERR_UNSUPPORTED;
+  size_t need = 0;
+  st = switch_layer_norm_residual_backward_workspace_size(T, d, dtype, &need);
+  if (st != SWL_OK) return st;
+  if (workspace_bytes < need) return SWL_ERR_WORKSPACE;
+  // what is written must not lie on what is read or on one another; dx may be dr
+  struct Span {
+    const void* p;
+    size_t n;
+  };
+  const size_t n = static_cast<size_t>(T) * d * e, nd = static_cast<size_t>(d) * 4, nt = static_cast<size_t>(T) * 4;
+  const Span out[9] = {{o.dx, n}, {o.dy, n}, {o.dgate, nt}, {sums[0], nd}, {sums[1], nd},
+                       {sums[2], nd}, {sums[3], nd}, {sums[4], nd}, {workspace, need}};
+  const Span read[10] = {{dr, n}, {dh, n}, {r, pre ? n : 0}, {y, n}, {gate, nt}, {norm->w_pre, nd},
+                         {norm->b_pre, nd}, {norm->w_post, nd}, {norm->b_post, nd}, {norm->scale, nd}};
+  for (int i = 0; i < 9; ++i) {
+    for (int j = 0; j < i; ++j)
+      if (meet(out[i].p, out[i].n, out[j].p, out[j].n)) return SWL_ERR_INVALID_ARG;
+    for (int j = 0; j < 10; ++j)
+      if (meet(out[i].p, out[i].n, read[j].p, read[j].n) && !(i == 0 && j == 0 && o.dx == dr))
+        return SWL_ERR_INVALID_ARG;
+  }
+  const int sms = sm_count();
+  if (sms <= 0) return SWL_ERR_CUDA;
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  SumArgs s = {static_cast<const float*>(workspace), {}, 0, static_cast<int>(d)};
+  unsigned wanted = 0;
+  for (int i = 0; i < kSums; ++i) {
+    s.out[i] = sums[i];
+    wanted |= sums[i] ? 1u << i : 0u;
+  }
+  if (T > 0) {
+    const Plan q = make_plan(d, dtype, {dr, dh, pre ? r : nullptr, y, o.dx, o.dy},
+                             {norm->w_pre, norm->b_pre, norm->w_post, norm->b_post, norm->scale});
+    const BwdArgsN a = {params_of(T, d, norm, gate, q.W), dr, dh, r, y, o.dx, o.dy, o.dgate,
+                        static_cast<float*>(workspace), wanted};
+    const int64_t want = (T + q.groups - 1) / q.groups;
+    const int64_t most = static_cast<int64_t>(sms < kMaxSms ? sms : kMaxSms) * (q.threads <= 256 ? kBwdCtasPerSm : 1);
+    s.parts = static_cast<int>(want < most ? want : most);
+    RunBwd run = {a, q, s.parts, cs};
+    if (!dispatch(q, dtype, norm->kind == SWL_NORM_LAYER, run)) return SWL_ERR_CUDA;
+    count_launch();
+  }
+  if (wanted) {
+    if (launch_dependent(norm_residual_sum_kernel, dim3(static_cast<unsigned>((d + 31) / 32), kSums),
+                         dim3(512), 0, cs, s) != cudaSuccess)
+      return SWL_ERR_CUDA;
+    count_launch();
+  }
+  return SWL_OK;
+}

@@ -74,3 +74,76 @@ def test_adamw_refuses_bad_calls(L):
     assert L.switch_layer_adamw_step(None, 1, ctypes.byref(swl.Adamw(1e-3, .9, .9, 1e-8, 0)),
                                      0x100000, None, None, None) == INVALID
     assert L.switch_layer_adamw_step(None, 0, None, 0x100000, None, None, None) == INVALID
+
+
+# ---------------------------------------------------------------- norms around a block
+def _norm(L, T=4, d=64, dtype=swl.SWL_BF16, kind=0, eps=1e-6, change=None, norm=None):
+    a = dict(x=0x10000, y=0x20000, gate=0x30000, r=0x40000, h=0x50000)
+    n = dict(w_pre=0x61000, w_post=0x62000, scale=0x63000)
+    a.update(change or {})
+    n.update(norm or {})
+    s = swl.Norm(kind, eps, n.get("w_pre"), n.get("b_pre"), n.get("w_post"), n.get("b_post"),
+                 n.get("scale"))
+    before = L.switch_layer_launch_count()
+    st = L.switch_layer_norm_residual(T, d, dtype, a["x"], a["y"], a["gate"], ctypes.byref(s),
+                                      a["r"], a["h"], None)
+    assert L.switch_layer_launch_count() == before
+    return st
+
+
+def test_norm_residual_refusals(L):
+    for kw in (dict(T=-1), dict(d=0), dict(dtype=5), dict(kind=2), dict(eps=0.0),
+               dict(eps=float("nan")), dict(norm=dict(b_pre=0x64000)), dict(change=dict(x=None)),
+               dict(change=dict(r=None)), dict(change=dict(y=None)), dict(change=dict(h=None)),
+               dict(norm=dict(w_pre=None)), dict(change=dict(r=0x50000)),      # r is h
+               dict(change=dict(r=0x10100)), dict(change=dict(h=0x20002)),     # across x, y
+               dict(change=dict(h=0x61000)), dict(change=dict(r=0x30000)),     # on w_pre, gate
+               dict(kind=1, norm=dict(w_post=None, b_post=0x64000))):
+        assert _norm(L, **kw) == INVALID, kw
+    for kw in (dict(d=16385), dict(change=dict(x=0x10001)), dict(change=dict(gate=0x30002)),
+               dict(norm=dict(scale=0x63002)), dict(dtype=swl.SWL_F32, change=dict(h=0x50002))):
+        assert _norm(L, **kw) == UNSUPPORTED, kw
+    assert L.switch_layer_norm_residual(4, 64, 1, 0x10000, None, None, None, None, 0x50000,
+                                        None) == INVALID
+    assert _norm(L, T=0) == OK                       # an empty batch: nothing to do
+
+
+def _norm_bwd(L, T=4, d=64, change=None, norm=None, out=None, ws=0x100000, ws_bytes=1 << 20,
+              kind=0):
+    a = dict(dr=0x10000, dh=0x11000, r=0x12000, y=0x13000, gate=0x14000)
+    n = dict(w_pre=0x21000, w_post=0x22000, scale=0x23000)
+    o = dict(dx=0x30000, dy=0x31000, dgate=0x32000, dw_pre=0x33000, dw_post=0x34000,
+             dscale=0x35000)
+    a.update(change or {})
+    n.update(norm or {})
+    o.update(out or {})
+    s = swl.Norm(kind, 1e-6, n.get("w_pre"), n.get("b_pre"), n.get("w_post"), n.get("b_post"),
+                 n.get("scale"))
+    g = swl.NormGrads(**o)
+    before = L.switch_layer_launch_count()
+    st = L.switch_layer_norm_residual_backward(T, d, 1, a["dr"], a["dh"], a["r"], a["y"],
+                                               a["gate"], ctypes.byref(s), ctypes.byref(g), ws,
+                                               ws_bytes, None)
+    assert L.switch_layer_launch_count() == before
+    return st
+
+
+def test_norm_residual_backward_refusals(L):
+    for kw in (dict(change=dict(dh=None)), dict(change=dict(r=None)), dict(out=dict(dx=None)),
+               dict(out=dict(dy=None)), dict(change=dict(y=None)), dict(norm=dict(w_pre=None)),
+               dict(change=dict(gate=None)), dict(out=dict(db_pre=0x36000)),
+               dict(norm=dict(scale=None)), dict(ws=None), dict(out=dict(dy=0x30000)),
+               dict(out=dict(dx=0x11000)), dict(out=dict(dx=0x10002)), dict(out=dict(dscale=0x33004)),
+               dict(out=dict(dw_pre=0x21000)), dict(ws=0x12000), dict(out=dict(dgate=0x14000)),
+               dict(norm=dict(w_pre=None, w_post=None, scale=None),
+                    change=dict(dr=None, dh=None), out=dict(dw_pre=None, dw_post=None, dscale=None))):
+        assert _norm_bwd(L, **kw) == INVALID, kw
+    for kw in (dict(d=20000), dict(change=dict(dr=0x10001)), dict(out=dict(dw_pre=0x33002)),
+               dict(ws=0x100010)):
+        assert _norm_bwd(L, **kw) == UNSUPPORTED, kw
+    assert _norm_bwd(L, ws_bytes=64) == WORKSPACE
+    n = ctypes.c_size_t()
+    size = L.switch_layer_norm_residual_backward_workspace_size
+    assert size(10, 64, 1, ctypes.byref(n)) == OK and n.value == 10 * 5 * 64 * 4
+    assert size(1 << 30, 64, 1, ctypes.byref(n)) == OK and n.value < 1 << 20
+    assert size(10, 64, 1, None) == INVALID and size(10, 1 << 20, 0, ctypes.byref(n)) == UNSUPPORTED
