@@ -19,10 +19,12 @@
 //
 // Bound: HBM, one read of every input row and one write of every output row
 // (forward 4, backward 6 row-sized arrays).  A row is held in registers by a group
-// of W warps (E elements per thread, 16 bytes per load where widths and pointers
-// allow); sums over the row go through warp shuffles and, for W > 1, one
-// exchange in shared memory behind a barrier of the group alone, so several rows
-// are in flight per SM without waiting for one another.  All sums are fp32, a
+// of `span` threads (E elements each, 16 bytes per load where widths and pointers
+// allow); sums over the row go through warp shuffles and, for rows wider than a
+// warp, one exchange in shared memory behind a barrier of the group alone, so
+// several rows are in flight per SM without waiting for one another.  The rows
+// ahead are copied to shared memory by cp.async, each thread its own columns, so no
+// thread waits for another's copy and no registers hold what is in flight.  All sums are fp32, a
 // layer norm's variance is taken about the mean in a second sum.  The parameters'
 // gradients are column sums over all rows: a thread keeps its columns' sums in
 // registers over all the rows it sees (grid-stride), the groups of a CTA add theirs
@@ -40,7 +42,7 @@ namespace swl {
 namespace {
 
 constexpr int kMaxWarps = 16;         // warps per row, at most
-constexpr int kMaxWidth = 16384;      // 16 warps x 32 lanes x 32 elements
+constexpr int kMaxWidth = 16384;      // 512 threads x 32 elements
 constexpr int kSums = 5;              // column sums: w_pre, b_pre, w_post, b_post, scale
 
 template <typename T, int V>
@@ -109,7 +111,7 @@ struct Params {
   float eps, inv_d;
   int d;
   int64_t T;
-  int W;              // warps per row (a power of two)
+  int span;           // threads per row (a power of two)
 };
 struct FwdArgs {
   Params p;
@@ -132,12 +134,12 @@ struct BwdArgsN {
 };
 
 // A thread's place: its group's rows and its own columns (vector k starts at
-// column (k * 32 W + tid) * V).
+// column (k * span + tid) * V).
 template <int V, int E>
 struct Lane {
   int tid, group, groups, span;     // span: threads of a group
-  __device__ __forceinline__ explicit Lane(int W) {
-    span = 32 * W;
+  __device__ __forceinline__ explicit Lane(int threads_per_row) {
+    span = threads_per_row;
     group = threadIdx.x / span;
     tid = threadIdx.x - group * span;
     groups = blockDim.x / span;
@@ -148,12 +150,13 @@ struct Lane {
 template <typename T, int V, int E>
 struct Row {
   Vec<T, V> v[E / V];
-  __device__ __forceinline__ void load(const void* base, int64_t row, int d, const Lane<V, E>& l) {
+  __device__ __forceinline__ void load(const void* base, int64_t row, bool valid, int d,
+                                       const Lane<V, E>& l) {
     const T* p = static_cast<const T*>(base) + row * d;
 #pragma unroll
     for (int k = 0; k < E / V; ++k) {
       const int c = l.col(k);
-      if (c < d) v[k].q = *reinterpret_cast<const decltype(v[k].q)*>(p + c);
+      if (valid && c < d) v[k].q = *reinterpret_cast<const decltype(v[k].q)*>(p + c);
       else v[k].q = decltype(v[k].q){};
     }
   }
@@ -162,16 +165,77 @@ struct Row {
     for (int k = 0; k < E / V; ++k) v[k].get(o + k * V);
   }
 };
+
+// The rows ahead of the one being worked on, kStages - 1 of them, for A arrays:
+// vector k of array a of a stage lies at [(stage A + a) E / V + k][thread].  Every
+// thread copies and reads its own columns only.  Vectors under 4 bytes (cp.async
+// has none) and rows too wide for shared memory are loaded where they are used.
+constexpr int kStages = 3;
 template <typename T, int V, int E>
-__device__ __forceinline__ void store_row(void* base, int64_t row, int d, const Lane<V, E>& l,
-                                          const float (&o)[E]) {
+constexpr bool use_ring() {
+  return sizeof(T) * V >= 4 && sizeof(T) * E <= 32;
+}
+template <typename T, int V, int E, int A>
+struct Ring {
+  static constexpr int kBytes = sizeof(T) * V;
+  static constexpr bool kOn = use_ring<T, V, E>();
+  unsigned char* smem;
+  uint32_t base;
+  int fill = 0, take = 0;
+  __device__ __forceinline__ explicit Ring(unsigned char* s)
+      : smem(s), base(static_cast<uint32_t>(__cvta_generic_to_shared(s))) {}
+  __device__ __forceinline__ int slot(int stage, int a, int k) const {
+    return (((stage * A + a) * (E / V) + k) * static_cast<int>(blockDim.x) +
+            static_cast<int>(threadIdx.x)) * kBytes;
+  }
+  __device__ __forceinline__ void put(int a, const void* src, int64_t row, bool valid, int d,
+                                      const Lane<V, E>& l) const {
+    const T* p = static_cast<const T*>(src) + row * d;
+#pragma unroll
+    for (int k = 0; k < E / V; ++k) {
+      const int c = l.col(k);
+      const bool in = valid && c < d;
+      // zero bytes are read (and the slot zero-filled) past the row and past T
+      const T* from = in ? p + c : static_cast<const T*>(src);
+      const int n = in ? kBytes : 0;
+      if constexpr (kBytes == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(base + slot(fill, a, k)),
+                     "l"(from), "r"(n)
+                     : "memory");
+      else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(base + slot(fill, a, k)),
+                     "l"(from), "n"(kBytes < 4 ? 4 : kBytes), "r"(n)
+                     : "memory");
+    }
+  }
+  __device__ __forceinline__ void commit() {
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    fill = fill + 1 == kStages ? 0 : fill + 1;
+  }
+  __device__ __forceinline__ void wait() const {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+  }
+  __device__ __forceinline__ void get(int a, float (&o)[E]) const {
+#pragma unroll
+    for (int k = 0; k < E / V; ++k) {
+      Vec<T, V> v;
+      v.q = *reinterpret_cast<const decltype(v.q)*>(smem + slot(take, a, k));
+      v.get(o + k * V);
+    }
+  }
+  __device__ __forceinline__ void next() { take = take + 1 == kStages ? 0 : take + 1; }
+};
+
+template <typename T, int V, int E>
+__device__ __forceinline__ void store_row(void* base, int64_t row, bool valid, int d,
+                                          const Lane<V, E>& l, const float (&o)[E]) {
   T* p = static_cast<T*>(base) + row * d;
 #pragma unroll
   for (int k = 0; k < E / V; ++k) {
     const int c = l.col(k);
     Vec<T, V> v;
     v.set(o + k * V);
-    if (c < d) *reinterpret_cast<decltype(v.q)*>(p + c) = v.q;
+    if (valid && c < d) *reinterpret_cast<decltype(v.q)*>(p + c) = v.q;
   }
 }
 // A parameter vector's values at this thread's columns (fp32; the loads hit L1).
@@ -185,51 +249,63 @@ __device__ __forceinline__ void load_param(const float* p, int d, const Lane<V, 
 #pragma unroll
     for (int i = 0; i < V; i += F) {
       Vec<float, F> v;
-      if (c < d) {
-        v.q = __ldg(reinterpret_cast<const decltype(v.q)*>(p + c + i));
-        v.get(o + k * V + i);
-      } else {
+      v.q = decltype(v.q){};
+      if (c < d) v.q = __ldg(reinterpret_cast<const decltype(v.q)*>(p + c + i));
+      v.get(o + k * V + i);
+    }
+  }
+}
+
+// Sums over the row of N values per thread, the same in every thread of the
+// group.  The two buffers alternate, so one barrier per sum is enough: a thread
+// that writes a buffer again has passed the next sum's barrier, which follows
+// every read.
+template <int N>
+__device__ __forceinline__ void row_sum(float (&v)[N], int span, float (*buf)[4][kMaxWarps],
+                                        int& turn) {
+  if (span < 32) {
+    for (int o = span >> 1; o > 0; o >>= 1)
 #pragma unroll
-        for (int j = 0; j < F; ++j) o[k * V + i + j] = 0.f;
+      for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+    return;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+  if (span == 32) return;
+  const int warps = span >> 5, warp = threadIdx.x >> 5;
+  const int group = threadIdx.x / span, first = group * warps;
+  float(*b)[kMaxWarps] = buf[turn];
+  turn ^= 1;
+  if ((threadIdx.x & 31) == 0)
+#pragma unroll
+    for (int i = 0; i < N; ++i) b[i][warp] = v[i];
+  asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(span) : "memory");
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    if (warps == 2) {
+      const float2 q = *reinterpret_cast<const float2*>(&b[i][first]);
+      v[i] = q.x + q.y;
+    } else {
+      v[i] = 0.f;
+      for (int w = 0; w < warps; w += 4) {
+        const float4 q = *reinterpret_cast<const float4*>(&b[i][first + w]);
+        v[i] += (q.x + q.y) + (q.z + q.w);
       }
     }
   }
 }
 
-// Sums over the row of N values per thread, the same in every thread.  The two
-// buffers alternate, so one barrier per sum is enough: a thread that writes a
-// buffer again has passed the next sum's barrier, which follows every read.
-template <int N>
-__device__ __forceinline__ void row_sum(float (&v)[N], int W, float (*buf)[kMaxWarps][4],
-                                        int& turn) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
-#pragma unroll
-    for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
-  if (W == 1) return;
-  const int warp = threadIdx.x >> 5, group = warp / W;
-  float(*b)[4] = buf[turn];
-  turn ^= 1;
-  if ((threadIdx.x & 31) == 0)
-#pragma unroll
-    for (int i = 0; i < N; ++i) b[warp][i] = v[i];
-  asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(32 * W) : "memory");
-#pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = 0.f;
-  for (int w = 0; w < W; ++w)
-#pragma unroll
-    for (int i = 0; i < N; ++i) v[i] += b[group * W + w][i];
-}
-
 // v becomes v - mu (layer norm; v itself for RMS norm); returns rho.
 template <bool kLayer, int V, int E>
 __device__ __forceinline__ float center(float (&v)[E], const Params& p, const Lane<V, E>& l,
-                                        float (*buf)[kMaxWarps][4], int& turn) {
+                                        float (*buf)[4][kMaxWarps], int& turn) {
   if constexpr (kLayer) {
     float s[1] = {0.f};
 #pragma unroll
     for (int i = 0; i < E; ++i) s[0] += v[i];       // columns past d hold zeros
-    row_sum(s, p.W, buf, turn);
+    row_sum(s, p.span, buf, turn);
     const float mu = s[0] * p.inv_d;
 #pragma unroll
     for (int i = 0; i < E; ++i) v[i] = l.col(i / V) < p.d ? v[i] - mu : 0.f;
@@ -237,44 +313,68 @@ __device__ __forceinline__ float center(float (&v)[E], const Params& p, const La
   float s[1] = {0.f};
 #pragma unroll
   for (int i = 0; i < E; ++i) s[0] = fmaf(v[i], v[i], s[0]);
-  row_sum(s, p.W, buf, turn);
-  return 1.f / sqrtf(s[0] * p.inv_d + p.eps);
+  row_sum(s, p.span, buf, turn);
+  return rsqrtf(fmaf(s[0], p.inv_d, p.eps));
 }
 
-template <typename T, int V, int E, bool kLayer>
-__global__ void __launch_bounds__(512, 1)
+template <typename T, int V, int E, int kThreads, bool kLayer>
+__global__ void __launch_bounds__(kThreads, kThreads == 256 ? 3 : 1)
 norm_residual_kernel(const __grid_constant__ FwdArgs a) {
-  __shared__ float buf[2][kMaxWarps][4];
+  extern __shared__ __align__(16) unsigned char smem[];
+  __shared__ __align__(16) float buf[2][4][kMaxWarps];
   const Params& p = a.p;
-  const Lane<V, E> l(p.W);
+  const Lane<V, E> l(p.span);
+  using R = Ring<T, V, E, 2>;
+  R ring(smem);
   const int64_t stride = static_cast<int64_t>(gridDim.x) * l.groups;
-  int64_t row = static_cast<int64_t>(blockIdx.x) * l.groups + l.group;
+  // every group of a CTA takes the same number of steps (a warp may hold several groups)
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * l.groups;
   int turn = 0;
-  Row<T, V, E> qx, qy;
-  float gate = 1.f;
   auto fetch = [&](int64_t t) {
-    qx.load(a.x, t, p.d, l);
-    if (a.y) qy.load(a.y, t, p.d, l);
-    if (p.gate) gate = p.gate[t];
+    if (t < p.T + l.groups) {      // (past the last row nothing is read)
+      ring.put(0, a.x, t, t < p.T, p.d, l);
+      if (a.y) ring.put(1, a.y, t, t < p.T, p.d, l);
+    }
+    ring.commit();
   };
-  if (row < p.T) fetch(row);
-  for (; row < p.T; row += stride) {
-    float r[E], w[E];
-    qx.get(r);
-    float u[E];
-    const float g = gate;
-    if (a.y) qy.get(u);
-    if (row + stride < p.T) fetch(row + stride);     // the next row, under this row's sums
+  if constexpr (R::kOn) {
+#pragma unroll
+    for (int s = 0; s < kStages - 1; ++s) fetch(first + l.group + s * stride);
+  }
+  for (int64_t base = first; base < p.T; base += stride) {
+    const int64_t row = base + l.group;
+    const bool valid = row < p.T;
+    const float g = p.gate && valid ? p.gate[row] : 1.f;
+    float r[E], u[E], w[E];
+    if constexpr (R::kOn) {
+      ring.wait();
+      ring.get(0, r);
+      if (a.y) ring.get(1, u);
+      ring.next();
+      fetch(row + (kStages - 1) * stride);     // into the stage read in the last step
+    } else {
+      Row<T, V, E> q;
+      q.load(a.x, row, valid, p.d, l);
+      q.get(r);
+      if (a.y) {
+        q.load(a.y, row, valid, p.d, l);
+        q.get(u);
+      }
+    }
     if (a.y) {
+      float f = g;
       if (p.w_post) {
         const float rho = center<kLayer>(u, p, l, buf, turn);
         load_param(p.w_post, p.d, l, w);
-#pragma unroll
-        for (int i = 0; i < E; ++i) u[i] = u[i] * rho * w[i];
         if (kLayer && p.b_post) {
-          load_param(p.b_post, p.d, l, w);
+          float b[E];
+          load_param(p.b_post, p.d, l, b);
 #pragma unroll
-          for (int i = 0; i < E; ++i) u[i] += w[i];
+          for (int i = 0; i < E; ++i) u[i] = fmaf(u[i] * rho, w[i], b[i]);
+        } else {
+          f *= rho;
+#pragma unroll
+          for (int i = 0; i < E; ++i) u[i] *= w[i];
         }
       }
       if (p.scale) {
@@ -283,29 +383,31 @@ norm_residual_kernel(const __grid_constant__ FwdArgs a) {
         for (int i = 0; i < E; ++i) u[i] *= w[i];
       }
 #pragma unroll
-      for (int i = 0; i < E; ++i) r[i] = fmaf(g, u[i], r[i]);
-      store_row<T>(a.r, row, p.d, l, r);
+      for (int i = 0; i < E; ++i) r[i] = fmaf(f, u[i], r[i]);
+      store_row<T>(a.r, row, valid, p.d, l, r);
     }
     if (a.h) {
       const float rho = center<kLayer>(r, p, l, buf, turn);
       load_param(p.w_pre, p.d, l, w);
-#pragma unroll
-      for (int i = 0; i < E; ++i) r[i] = r[i] * rho * w[i];
       if (kLayer && p.b_pre) {
-        load_param(p.b_pre, p.d, l, w);
+        load_param(p.b_pre, p.d, l, u);
 #pragma unroll
-        for (int i = 0; i < E; ++i) r[i] += w[i];
+        for (int i = 0; i < E; ++i) r[i] = fmaf(r[i] * rho, w[i], u[i]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < E; ++i) r[i] = r[i] * rho * w[i];
       }
-      store_row<T>(a.h, row, p.d, l, r);
+      store_row<T>(a.h, row, valid, p.d, l, r);
     }
   }
+  if constexpr (R::kOn) asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
 // Row statistics of the backward pass: v becomes v - mu; returns rho, and
 // (through m0, m1) mean(a) and mean(a (v - mu)).
 template <bool kLayer, int V, int E>
 __device__ __forceinline__ float center_with(float (&v)[E], const float (&a)[E], const Params& p,
-                                             const Lane<V, E>& l, float (*buf)[kMaxWarps][4],
+                                             const Lane<V, E>& l, float (*buf)[4][kMaxWarps],
                                              int& turn, float& m0, float& m1) {
   m0 = 0.f;
   if constexpr (kLayer) {
@@ -315,7 +417,7 @@ __device__ __forceinline__ float center_with(float (&v)[E], const float (&a)[E],
       s[0] += v[i];
       s[1] += a[i];
     }
-    row_sum(s, p.W, buf, turn);
+    row_sum(s, p.span, buf, turn);
     const float mu = s[0] * p.inv_d;
     m0 = s[1] * p.inv_d;
 #pragma unroll
@@ -327,52 +429,70 @@ __device__ __forceinline__ float center_with(float (&v)[E], const float (&a)[E],
     s[0] = fmaf(v[i], v[i], s[0]);
     s[1] = fmaf(a[i], v[i], s[1]);
   }
-  row_sum(s, p.W, buf, turn);
+  row_sum(s, p.span, buf, turn);
   m1 = s[1] * p.inv_d;
-  return 1.f / sqrtf(s[0] * p.inv_d + p.eps);
+  return rsqrtf(fmaf(s[0], p.inv_d, p.eps));
 }
 
-template <typename T, int V, int E, bool kLayer>
-__global__ void __launch_bounds__(512, 1)
+template <typename T, int V, int E, int kThreads, bool kLayer>
+__global__ void __launch_bounds__(kThreads, kThreads == 256 ? 2 : 1)
 norm_residual_bwd_kernel(const __grid_constant__ BwdArgsN a) {
-  extern __shared__ float columns[];        // [d], when a CTA has several groups
-  __shared__ float buf[2][kMaxWarps][4];
+  extern __shared__ __align__(16) unsigned char smem[];
+  __shared__ __align__(16) float buf[2][4][kMaxWarps];
   const Params& p = a.p;
-  const Lane<V, E> l(p.W);
+  const Lane<V, E> l(p.span);
+  using R = Ring<T, V, E, 4>;
+  R ring(smem);
   pdl_trigger();
   const int64_t stride = static_cast<int64_t>(gridDim.x) * l.groups;
-  int64_t row = static_cast<int64_t>(blockIdx.x) * l.groups + l.group;
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * l.groups;
   int turn = 0;
   float acc[kSums][E];      // (RMS norm: the two bias sums are never touched)
 #pragma unroll
   for (int s = 0; s < kSums; ++s)
 #pragma unroll
     for (int i = 0; i < E; ++i) acc[s][i] = 0.f;
-  Row<T, V, E> qr, qh, qv, qy;
   auto fetch = [&](int64_t t) {
-    if (a.dr) qr.load(a.dr, t, p.d, l);
-    if (a.dh) {
-      qh.load(a.dh, t, p.d, l);
-      qv.load(a.r, t, p.d, l);
+    if (t < p.T + l.groups) {
+      const bool in = t < p.T;
+      if (a.dr) ring.put(0, a.dr, t, in, p.d, l);
+      if (a.dh) {
+        ring.put(1, a.dh, t, in, p.d, l);
+        ring.put(2, a.r, t, in, p.d, l);
+      }
+      if (a.y) ring.put(3, a.y, t, in, p.d, l);
     }
-    if (a.y) qy.load(a.y, t, p.d, l);
+    ring.commit();
   };
-  if (row < p.T) fetch(row);
-  for (; row < p.T; row += stride) {
-    float D[E], w[E];
+  if constexpr (R::kOn) {
+#pragma unroll
+    for (int s = 0; s < kStages - 1; ++s) fetch(first + l.group + s * stride);
+  }
+  for (int64_t base = first; base < p.T; base += stride) {
+    const int64_t row = base + l.group;
+    const bool valid = row < p.T;
+    float D[E], w[E], g[E], v[E], y[E];
+    // dx may be dr: a row's dr is read here, before its dx is written
+    auto take = [&](int k, const void* src, float (&o)[E]) {
+      if constexpr (R::kOn) {
+        ring.get(k, o);
+      } else {
+        Row<T, V, E> q;
+        q.load(src, row, valid, p.d, l);
+        q.get(o);
+      }
+    };
+    if constexpr (R::kOn) ring.wait();
     if (a.dr) {
-      qr.get(D);
+      take(0, a.dr, D);
     } else {
 #pragma unroll
       for (int i = 0; i < E; ++i) D[i] = 0.f;
     }
-    float g[E], v[E], y[E];
     if (a.dh) {
-      qh.get(g);
-      qv.get(v);
+      take(1, a.dh, g);
+      take(2, a.r, v);
     }
-    if (a.y) qy.get(y);
-    if (row + stride < p.T) fetch(row + stride);
     if (a.dh) {
       load_param(p.w_pre, p.d, l, w);
       if constexpr (kLayer) {
@@ -392,9 +512,14 @@ norm_residual_bwd_kernel(const __grid_constant__ BwdArgsN a) {
         D[i] = fmaf(t, rho, D[i]);
       }
     }
-    store_row<T>(a.dx, row, p.d, l, D);
+    store_row<T>(a.dx, row, valid, p.d, l, D);
+    if (a.y) take(3, a.y, y);
+    if constexpr (R::kOn) {
+      ring.next();
+      fetch(row + (kStages - 1) * stride);     // into the stage read in the last step
+    }
     if (!a.y) continue;
-    const float gate = p.gate ? p.gate[row] : 1.f;
+    const float gate = p.gate && valid ? p.gate[row] : 1.f;
     // D becomes scale . D (no gate): the gate's gradient needs it without the gate
     float sD[E];
     if (p.scale) {
@@ -431,13 +556,13 @@ norm_residual_bwd_kernel(const __grid_constant__ BwdArgsN a) {
         y[i] = hat;
       }
       if constexpr (kLayer) {
-        row_sum(s, p.W, buf, turn);
+        row_sum(s, p.span, buf, turn);
       } else {
         float one[1] = {s[1]};
-        row_sum(one, p.W, buf, turn);
+        row_sum(one, p.span, buf, turn);
         s[1] = one[0];
       }
-      if (a.dgate && l.tid == 0) a.dgate[row] = s[1] + s[2];
+      if (a.dgate && valid && l.tid == 0) a.dgate[row] = s[1] + s[2];
       const float m0 = s[0] * p.inv_d, m1 = s[1] * p.inv_d, f = gate * rho;
 #pragma unroll
       for (int i = 0; i < E; ++i) sD[i] = ((kLayer ? sD[i] - m0 : sD[i]) - y[i] * m1) * f;
@@ -450,12 +575,15 @@ norm_residual_bwd_kernel(const __grid_constant__ BwdArgsN a) {
         sD[i] *= gate;
       }
       if (a.dgate) {
-        row_sum(s, p.W, buf, turn);
-        if (l.tid == 0) a.dgate[row] = s[0];
+        row_sum(s, p.span, buf, turn);
+        if (valid && l.tid == 0) a.dgate[row] = s[0];
       }
     }
-    store_row<T>(a.dy, row, p.d, l, sD);
+    store_row<T>(a.dy, row, valid, p.d, l, sD);
   }
+  if constexpr (R::kOn) asm volatile("cp.async.wait_all;" ::: "memory");
+  __syncthreads();
+  float* const columns = reinterpret_cast<float*>(smem);   // [d], the ring is done with
   // this CTA's column sums: its groups add theirs in order
   float* part = a.part + static_cast<size_t>(blockIdx.x) * kSums * p.d;
 #pragma unroll
@@ -507,13 +635,16 @@ norm_residual_sum_kernel(const __grid_constant__ SumArgs a) {
 
 // ---------------------------------------------------------------- host
 struct Plan {
-  int V, E, W, threads, groups;
+  int V, E, span, threads, groups;
 };
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
-// Rows of up to 4096 elements: 8 elements per thread; wider rows 16 or 32, since
-// a row has 16 warps at most.  `elems`: pointers into rows; `params`: fp32 vectors.
-Plan make_plan(int64_t d, int dtype, std::initializer_list<const void*> elems,
+// Elements per thread E and threads per row.  More elements per thread spread a
+// row's fixed work (sums, addresses) over more of them; fewer give a small batch more
+// threads and a layer norm's backward pass (five column sums per element) its
+// registers.  `elems`: pointers into rows; `params`: fp32 vectors.
+Plan make_plan(int64_t T, int64_t d, int dtype, bool small_e, int sms,
+               std::initializer_list<const void*> elems,
                std::initializer_list<const float*> params) {
   Plan q;
   const int full = dtype == SWL_BF16 ? 8 : 4;
@@ -526,37 +657,53 @@ Plan make_plan(int64_t d, int dtype, std::initializer_list<const void*> elems,
     return true;
   };
   q.V = fits(full) ? full : dtype == SWL_BF16 && fits(2) ? 2 : 1;
-  q.E = d <= 4096 ? 8 : d <= 8192 ? 16 : 32;
-  q.W = 1;
-  while (q.W * 32 * q.E < d) q.W *= 2;
-  q.threads = q.W <= 8 ? 256 : 32 * q.W;
-  q.groups = q.threads / (32 * q.W);
+  q.threads = 256;
+  // E = 16 (bf16) once its threads fill the GPU's SMs with two warps per scheduler
+  if (dtype == SWL_BF16 && d <= 4096) {
+    const bool wide = d > 2048 || (!small_e && q.V == 8 && d > 256 && T * (d / 16) >= sms * 256ll);
+    q.E = wide ? 16 : 8;
+  } else if (dtype == SWL_F32 && d <= 2048) {
+    q.E = 8;
+  } else {
+    q.threads = 512;
+    q.E = dtype == SWL_F32 && d <= 4096 ? 8 : d <= 8192 ? 16 : 32;
+  }
+  q.span = 8;
+  while (q.span * q.E < d) q.span *= 2;
+  q.groups = q.threads / q.span;
   return q;
 }
 
 template <typename F>
 bool dispatch(const Plan& q, int dtype, bool layer, F f) {
-#define SWL_E(T, V, L)                                        \
-  switch (q.E) {                                              \
-    case 8: return f.template run<T, V, 8, L>();              \
-    case 16: return f.template run<T, V, 16, L>();            \
-    default: return f.template run<T, V, 32, L>();            \
-  }
-#define SWL_L(T, V)                  \
-  if (layer) {                       \
-    SWL_E(T, V, true)                \
-  } else {                           \
-    SWL_E(T, V, false)               \
-  }
+#define SWL_L(T, V, E, H) \
+  return layer ? f.template run<T, V, E, H, true>() : f.template run<T, V, E, H, false>();
+#define SWL_V(T, V)                                      \
+  if (q.threads == 256) {                                \
+    if (q.E == 8) { SWL_L(T, V, 8, 256) }                \
+    if constexpr (sizeof(T) == 2) { SWL_L(T, V, 16, 256) } \
+  }                                                      \
+  if constexpr (sizeof(T) == 4)                          \
+    if (q.E == 8) { SWL_L(T, V, 8, 512) }                \
+  if (q.E == 16) { SWL_L(T, V, 16, 512) }                \
+  SWL_L(T, V, 32, 512)
   if (dtype == SWL_BF16) {
-    if (q.V == 8) { SWL_L(__nv_bfloat16, 8) }
-    if (q.V == 2) { SWL_L(__nv_bfloat16, 2) }
-    SWL_L(__nv_bfloat16, 1)
+    if (q.V == 8) { SWL_V(__nv_bfloat16, 8) }
+    if (q.V == 2) { SWL_V(__nv_bfloat16, 2) }
+    SWL_V(__nv_bfloat16, 1)
   }
-  if (q.V == 4) { SWL_L(float, 4) }
-  SWL_L(float, 1)
+  if (q.V == 4) { SWL_V(float, 4) }
+  SWL_V(float, 1)
+#undef SWL_V
 #undef SWL_L
-#undef SWL_E
+}
+
+// Shared memory beyond 48 KB (with the static arrays) has to be asked for.
+template <typename K>
+bool allow_smem(K kernel, size_t bytes) {
+  return bytes <= 40 * 1024 ||
+         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              static_cast<int>(bytes)) == cudaSuccess;
 }
 
 struct RunFwd {
@@ -564,9 +711,11 @@ struct RunFwd {
   const Plan& q;
   int grid;
   cudaStream_t st;
-  template <typename T, int V, int E, bool L>
+  template <typename T, int V, int E, int H, bool L>
   bool run() {
-    norm_residual_kernel<T, V, E, L><<<grid, q.threads, 0, st>>>(a);
+    const size_t smem = use_ring<T, V, E>() ? size_t{kStages} * 2 * H * E * sizeof(T) : 0;
+    if (!allow_smem(norm_residual_kernel<T, V, E, H, L>, smem)) return false;
+    norm_residual_kernel<T, V, E, H, L><<<grid, H, smem, st>>>(a);
     return cudaGetLastError() == cudaSuccess;
   }
 };
@@ -575,10 +724,12 @@ struct RunBwd {
   const Plan& q;
   int grid;
   cudaStream_t st;
-  template <typename T, int V, int E, bool L>
+  template <typename T, int V, int E, int H, bool L>
   bool run() {
-    const size_t smem = q.groups > 1 ? static_cast<size_t>(a.p.d) * 4 : 0;
-    norm_residual_bwd_kernel<T, V, E, L><<<grid, q.threads, smem, st>>>(a);
+    size_t smem = use_ring<T, V, E>() ? size_t{kStages} * 4 * H * E * sizeof(T) : 0;
+    if (q.groups > 1 && smem < static_cast<size_t>(a.p.d) * 4) smem = static_cast<size_t>(a.p.d) * 4;
+    if (!allow_smem(norm_residual_bwd_kernel<T, V, E, H, L>, smem)) return false;
+    norm_residual_bwd_kernel<T, V, E, H, L><<<grid, H, smem, st>>>(a);
     return cudaGetLastError() == cudaSuccess;
   }
 };
@@ -608,9 +759,9 @@ swl_status check(int64_t T, int64_t d, int dtype, const swl_norm* n, bool y, boo
   return SWL_OK;
 }
 
-Params params_of(int64_t T, int64_t d, const swl_norm* n, const float* gate, int W) {
+Params params_of(int64_t T, int64_t d, const swl_norm* n, const float* gate, int span) {
   return {n->w_pre, n->b_pre, n->w_post, n->b_post, n->scale, gate, n->eps,
-          static_cast<float>(1.0 / static_cast<double>(d)), static_cast<int>(d), T, W};
+          static_cast<float>(1.0 / static_cast<double>(d)), static_cast<int>(d), T, span};
 }
 
 // Do [a, a + na) and [b, b + nb) share a byte?  (NULL: no)
@@ -650,11 +801,11 @@ extern "C" swl_status switch_layer_norm_residual(int64_t T, int64_t d, int dtype
   }
   const int sms = sm_count();
   if (sms <= 0) return SWL_ERR_CUDA;
-  const Plan q = make_plan(d, dtype, {x, y, r, h},
+  const Plan q = make_plan(T, d, dtype, false, sms, {x, y, r, h},
                            {norm->w_pre, norm->b_pre, norm->w_post, norm->b_post, norm->scale});
-  const FwdArgs a = {params_of(T, d, norm, gate, q.W), x, y, r, h};
+  const FwdArgs a = {params_of(T, d, norm, gate, q.span), x, y, r, h};
   const int64_t want = (T + q.groups - 1) / q.groups;
-  const int64_t most = static_cast<int64_t>(sms) * (q.threads <= 256 ? 4 : 2);
+  const int64_t most = static_cast<int64_t>(sms) * (q.threads == 256 ? 3 : 1);
   RunFwd run = {a, q, static_cast<int>(want < most ? want : most), static_cast<cudaStream_t>(stream)};
   if (!dispatch(q, dtype, norm->kind == SWL_NORM_LAYER, run)) return SWL_ERR_CUDA;
   count_launch();
@@ -730,12 +881,12 @@ extern "C" swl_status switch_layer_norm_residual_backward(
     wanted |= sums[i] ? 1u << i : 0u;
   }
   if (T > 0) {
-    const Plan q = make_plan(d, dtype, {dr, dh, pre ? r : nullptr, y, o.dx, o.dy},
+    const Plan q = make_plan(T, d, dtype, norm->kind == SWL_NORM_LAYER, sms, {dr, dh, pre ? r : nullptr, y, o.dx, o.dy},
                              {norm->w_pre, norm->b_pre, norm->w_post, norm->b_post, norm->scale});
-    const BwdArgsN a = {params_of(T, d, norm, gate, q.W), dr, dh, r, y, o.dx, o.dy, o.dgate,
+    const BwdArgsN a = {params_of(T, d, norm, gate, q.span), dr, dh, r, y, o.dx, o.dy, o.dgate,
                         static_cast<float*>(workspace), wanted};
     const int64_t want = (T + q.groups - 1) / q.groups;
-    const int64_t most = static_cast<int64_t>(sms < kMaxSms ? sms : kMaxSms) * (q.threads <= 256 ? kBwdCtasPerSm : 1);
+    const int64_t most = static_cast<int64_t>(sms < kMaxSms ? sms : kMaxSms) * (q.threads == 256 ? kBwdCtasPerSm : 1);
     s.parts = static_cast<int>(want < most ? want : most);
     RunBwd run = {a, q, s.parts, cs};
     if (!dispatch(q, dtype, norm->kind == SWL_NORM_LAYER, run)) return SWL_ERR_CUDA;
