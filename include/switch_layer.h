@@ -246,6 +246,38 @@ swl_status switch_layer_forward_variant(int64_t T, int64_t d, int64_t d_ff, int6
                                         const float* b_r, const swl_variant* variant,
                                         void* workspace, size_t workspace_bytes, void* stream);
 
+/* ---- Products grouped by expert over ragged row ranges ----
+ * The experts' products for experts of the caller's own design (another activation,
+ * no capacity cut, a training step of its own), between a dispatch that packs the
+ * token rows by expert and a combine.  Group e owns the rows
+ * offsets[e] <= r < offsets[e + 1]:
+ *   y[r]  = W[e] x[r] + bias[e]
+ *   dx[r] = W[e]^T dy[r],  dW[e] = sum_r dy[r] x[r]^T,  db[e] = sum_r dy[r]
+ *   R, K, O, N   rows of the buffers (R = 0: no rows), width of x, width of y, groups
+ *   x [R, K], y [R, O], W [N, O, K], bias [N, O] or NULL: dtype; products and sums are
+ *                fp32, each result rounded once
+ *   offsets      DEVICE int32 [N + 1], 0 <= offsets[0] <= ... <= offsets[N] <= R.  Rows
+ *                outside every group are neither read nor written: y and dx keep them.
+ *                Empty groups: no rows, and zero dW and db.
+ * The offsets are only on the device: offsets that break the rule write nothing and
+ * make switch_layer_device_status SWL_ERR_DEVICE, as does a pipeline wait that runs out.
+ * backward: dx, dW, db may each be NULL when not wanted (W is read for dx only, x for dW
+ * only); outputs are written, not added to.  Outputs and workspace overlap neither inputs
+ * nor each other (SWL_ERR_INVALID_ARG).  bf16 requires K % 8 == 0, O % 8 == 0 and 16-byte
+ * aligned x, y, W, dy, dx, dW (SWL_ERR_UNSUPPORTED), as the layer does.  workspace:
+ * switch_layer_grouped_workspace_size bytes, 256-byte aligned, no initialisation. */
+swl_status switch_layer_grouped_workspace_size(int64_t R, int64_t K, int64_t O, int64_t N,
+                                               int dtype, size_t* bytes);
+swl_status switch_layer_grouped_matmul(int64_t R, int64_t K, int64_t O, int64_t N, int dtype,
+                                       const void* x, const int32_t* offsets, const void* W,
+                                       const void* bias, void* y, void* workspace,
+                                       size_t workspace_bytes, void* stream);
+swl_status switch_layer_grouped_matmul_backward(int64_t R, int64_t K, int64_t O, int64_t N,
+                                                int dtype, const void* dy, const void* x,
+                                                const int32_t* offsets, const void* W, void* dx,
+                                                void* dW, void* db, void* workspace,
+                                                size_t workspace_bytes, void* stream);
+
 /* ---- The norms around a block, with its gate, residual scale and residual ----
  * The layer adds no residual; this does, with the norms on both sides:
  *   n(v; w, b) = (v - mu) / sqrt(mean((v - mu)^2) + eps) * w + b, with mu = mean(v)

@@ -50,7 +50,8 @@ EXPORTS = ("switch_layer_capacity", "switch_layer_workspace_size", "switch_layer
            "switch_layer_backward_workspace_size", "switch_layer_backward",
            "switch_layer_adamw_step", "switch_layer_norm_residual",
            "switch_layer_norm_residual_backward_workspace_size",
-           "switch_layer_norm_residual_backward")
+           "switch_layer_norm_residual_backward", "switch_layer_grouped_workspace_size",
+           "switch_layer_grouped_matmul", "switch_layer_grouped_matmul_backward")
 SWL_ACT_RELU, SWL_ACT_GEGLU = 0, 1
 
 
@@ -203,6 +204,15 @@ def lib() -> ctypes.CDLL:
     L.switch_layer_forward_shard_end.argtypes = [_i64, _i64, _i64, _i64, _i32, _i64, _i32,
                                                  _i32, _vp, _vp, _vp, _vp, _vp, _vp, _dbl,
                                                  _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]
+    L.switch_layer_grouped_workspace_size.restype = _i32
+    L.switch_layer_grouped_workspace_size.argtypes = [_i64, _i64, _i64, _i64, _i32,
+                                                      ctypes.POINTER(_sz)]
+    L.switch_layer_grouped_matmul.restype = _i32
+    L.switch_layer_grouped_matmul.argtypes = ([_i64, _i64, _i64, _i64, _i32] + [_vp] * 6 +
+                                              [_sz, _vp])
+    L.switch_layer_grouped_matmul_backward.restype = _i32
+    L.switch_layer_grouped_matmul_backward.argtypes = ([_i64, _i64, _i64, _i64, _i32] +
+                                                       [_vp] * 8 + [_sz, _vp])
     L.switch_layer_norm_residual.restype = _i32
     L.switch_layer_norm_residual.argtypes = [_i64, _i64, _i32, _vp, _vp, _vp,
                                              ctypes.POINTER(Norm), _vp, _vp, _vp]
@@ -826,6 +836,89 @@ def _allocating_on(stream, dev: torch.device):
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(int(stream), device=dev)
     return torch.cuda.stream(stream)
+
+
+# ---------------------------------------------------------------------------
+# products grouped by expert
+# ---------------------------------------------------------------------------
+def switch_layer_grouped_workspace_size(R, K, O, N, dtype: int) -> int:
+    n = _sz(0)
+    _check(lib().switch_layer_grouped_workspace_size(R, K, O, N, dtype, ctypes.byref(n)),
+           "grouped_workspace_size")
+    return int(n.value)
+
+
+def _grouped_workspace(workspace, R, K, O, N, dt, dev):
+    if workspace is None:
+        return torch.empty(switch_layer_grouped_workspace_size(R, K, O, N, dtype_code(dt)),
+                           dtype=torch.uint8, device=dev)
+    _require(workspace, "workspace", torch.uint8)
+    if workspace.device != dev:
+        raise ValueError("workspace is on %s: all tensors must be on %s" % (workspace.device, dev))
+    return workspace
+
+
+def grouped_matmul(x: torch.Tensor, offsets: torch.Tensor, W: torch.Tensor,
+                   bias: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                   workspace: Optional[torch.Tensor] = None, stream=None,
+                   check: bool = True) -> torch.Tensor:
+    """y [R, O]: ``y[r] = W[e] x[r] + bias[e]`` for the rows offsets[e] <= r < offsets[e + 1]
+    (see switch_layer_grouped_matmul in include/switch_layer.h).  Rows of no group keep what
+    ``out`` holds (zeros when it is allocated here)."""
+    if x.dim() != 2 or W.dim() != 3:
+        raise ValueError("x must be [R, K] and W [N, O, K]")
+    dev, dt = x.device, x.dtype
+    R, K = x.shape
+    N, O, _ = W.shape
+    px = _at(x, "x", dt, (R, K), dev)
+    pw = _at(W, "W", dt, (N, O, K), dev)
+    po = _at(offsets, "offsets", torch.int32, (N + 1,), dev)
+    pb = _at(bias, "bias", dt, (N, O), dev)
+    with _allocating_on(stream, dev):
+        if out is None:
+            out = torch.zeros((R, O), dtype=dt, device=dev)
+        ws = _grouped_workspace(workspace, R, K, O, N, dt, dev)
+    with _on(dev):
+        _check(lib().switch_layer_grouped_matmul(
+            R, K, O, N, dtype_code(dt), px, po, pw, pb, _at(out, "out", dt, (R, O), dev),
+            ws.data_ptr(), ws.numel(), _stream_handle(stream)), "grouped_matmul")
+        if check:
+            _check(switch_layer_device_status(ws, stream), "device status")
+    return out
+
+
+def grouped_matmul_backward(dy: torch.Tensor, x: torch.Tensor, offsets: torch.Tensor,
+                            W: torch.Tensor, dx: Optional[torch.Tensor] = None,
+                            dW: Optional[torch.Tensor] = None, db: Optional[torch.Tensor] = None,
+                            workspace: Optional[torch.Tensor] = None, stream=None,
+                            check: bool = True) -> dict:
+    """dx, dW and db of ``grouped_matmul`` for the gradient ``dy`` of its result.  With none
+    of the three given, all are allocated; otherwise only the given ones are computed (the
+    others are None in the result).  Rows of no group keep what ``dx`` holds (zeros when it
+    is allocated here)."""
+    if dy.dim() != 2 or x.dim() != 2 or W.dim() != 3:
+        raise ValueError("dy must be [R, O], x [R, K] and W [N, O, K]")
+    dev, dt = dy.device, dy.dtype
+    R, K = x.shape
+    N, O, _ = W.shape
+    pdy = _at(dy, "dy", dt, (R, O), dev)
+    px = _at(x, "x", dt, (R, K), dev)
+    pw = _at(W, "W", dt, (N, O, K), dev)
+    po = _at(offsets, "offsets", torch.int32, (N + 1,), dev)
+    with _allocating_on(stream, dev):
+        if dx is None and dW is None and db is None:
+            dx = torch.zeros((R, K), dtype=dt, device=dev)
+            dW = torch.empty((N, O, K), dtype=dt, device=dev)
+            db = torch.empty((N, O), dtype=dt, device=dev)
+        ws = _grouped_workspace(workspace, R, K, O, N, dt, dev)
+    with _on(dev):
+        _check(lib().switch_layer_grouped_matmul_backward(
+            R, K, O, N, dtype_code(dt), pdy, px, po, pw, _at(dx, "dx", dt, (R, K), dev),
+            _at(dW, "dW", dt, (N, O, K), dev), _at(db, "db", dt, (N, O), dev), ws.data_ptr(),
+            ws.numel(), _stream_handle(stream)), "grouped_matmul_backward")
+        if check:
+            _check(switch_layer_device_status(ws, stream), "device status")
+    return {"dx": dx, "dW": dW, "db": db}
 
 
 # ---------------------------------------------------------------------------

@@ -1,0 +1,487 @@
+// Products grouped by expert over ragged row ranges: the plan kernel, the
+// products on the CUDA cores, the bias gradient and the C entry points.
+//
+// Group e owns the rows offsets[e] <= r < offsets[e + 1] of x [R, K], y [R, O]:
+//   y[r]  = W[e] x[r] + b[e]                  W [N, O, K], b [N, O]
+//   dx[r] = W[e]^T dy[r]
+//   dW[e] = sum_r dy[r] x[r]^T,  db[e] = sum_r dy[r]
+// Rows outside every group are neither read nor written.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <climits>
+
+#include "grouped_products.h"
+#include "switch_layer.h"
+
+namespace swl {
+namespace {
+
+// ---------------------------------------------------------------- plan
+constexpr int kPlanThreads = 1024;
+
+// Inclusive sum over the CTA; every thread gets its own prefix, *total the sum.
+__device__ __forceinline__ int block_scan(int v, int* warp_sums, int* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += u;
+  }
+  if (lane == 31) warp_sums[warp] = v;
+  __syncthreads();
+  if (warp == 0) {
+    int s = warp_sums[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, s, o);
+      if (lane >= o) s += u;
+    }
+    warp_sums[lane] = s;
+  }
+  __syncthreads();
+  const int before = warp > 0 ? warp_sums[warp - 1] : 0;
+  *total = warp_sums[31];
+  __syncthreads();
+  return v + before;
+}
+
+// One CTA.  A group has at most R / tile_rows + 1 tiles, so the counts fit an int.
+__global__ void __launch_bounds__(kPlanThreads)
+grouped_plan_kernel(const int* __restrict__ off, int* __restrict__ prefix, WsHeader* hdr, int N,
+                    int R, int tile_rows) {
+  __shared__ int warp_sums[32];
+  pdl_trigger();
+  pdl_wait();
+  int base = 0;
+  bool bad = false;
+  for (int e0 = 0; e0 < N; e0 += kPlanThreads) {
+    const int e = e0 + static_cast<int>(threadIdx.x);
+    int tiles = 0;
+    if (e < N) {
+      const int a = off[e], b = off[e + 1];
+      if (a < 0 || b < a || b > R) bad = true;
+      else tiles = (b - a + tile_rows - 1) / tile_rows;
+    }
+    int total;
+    const int incl = block_scan(tiles, warp_sums, &total);
+    if (e < N) prefix[e + 1] = base + incl;
+    base += total;
+  }
+  if (__syncthreads_or(bad)) {      // the prefix says: nothing to do
+    for (int e = threadIdx.x; e <= N; e += kPlanThreads) prefix[e] = 0;
+    if (threadIdx.x == 0) hdr->err = kDevIndexOutOfRange;
+  } else if (threadIdx.x == 0) {
+    prefix[0] = 0;
+    hdr->err = kDevOk;
+  }
+  if (threadIdx.x == 0) hdr->next_tile = 0;
+}
+
+// Last e with P[e] <= q (P[N] > q).
+__device__ __forceinline__ int find_group(const int* __restrict__ P, int N, int q) {
+  int lo = 0, hi = N;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (P[mid] <= q) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+// ---------------------------------------------------------------- CUDA-core products
+// C[m, n] = sum_k A(m, k) B(n, k): a CTA of 16 x 16 threads computes a TM x 128
+// tile, TM / 16 x 8 values per thread, in steps of 16 along k.  The operands of a
+// step go through shared memory (k-major, two buffers); the next step's are read
+// into registers under the arithmetic.  Bound: fp32 FMA issue for full tiles
+// (TM = 128: 64 FMAs per four 16-byte shared loads); W's bytes for groups of a few
+// rows, for which the narrow tile (TM = 32) wastes fewer FMAs on missing rows.
+constexpr int kTN = 128, kTK = 16;
+constexpr int kSimtThreads = 256;
+
+template <typename T>
+struct SimtArgs {
+  const T* a;
+  const T* b;
+  const T* bias;
+  T* out;
+  const int* off;
+  const int* prefix;
+  const WsHeader* hdr;
+  int K, O, N;
+};
+
+template <typename T, int W, int TM>
+__global__ void __launch_bounds__(kSimtThreads, TM == 128 ? 2 : 3)
+grouped_simt_kernel(const __grid_constant__ SimtArgs<T> p) {
+  // k-contiguous operands: A for y and dx, B for y; else the tile's index is
+  constexpr bool kAk = W != kGroupedDw, kBk = W == kGroupedFwd;
+  constexpr int RM = TM / 16;
+  __shared__ __align__(16) float sA[2][kTK][TM + 4], sB[2][kTK][kTN + 4];
+  pdl_trigger();
+  pdl_wait();
+  const int tid = threadIdx.x;
+  const int tx = tid & 15, ty = tid >> 4;
+  const int n_cols = W == kGroupedFwd ? p.O : p.K;          // columns of the output
+  const int n_tiles = (n_cols + kTN - 1) / kTN;
+  const int m_tiles_w = (p.O + TM - 1) / TM;                // row tiles of dW[e]
+  const int total = W == kGroupedDw ? (p.hdr->err ? 0 : p.N * m_tiles_w * n_tiles)
+                                    : p.prefix[p.N] * n_tiles;
+  for (int t = blockIdx.x; t < total; t += gridDim.x) {
+    int e, m0, n0, m_end, row0 = 0, kn;
+    if constexpr (W == kGroupedDw) {
+      e = t / (m_tiles_w * n_tiles);
+      const int r = t - e * m_tiles_w * n_tiles;
+      m0 = r / n_tiles * TM;
+      n0 = (r % n_tiles) * kTN;
+      m_end = p.O;
+      row0 = p.off[e];
+      kn = p.off[e + 1] - row0;
+    } else {
+      // within a group: row tiles fastest, so the CTAs running together share W
+      const int q = t / n_tiles;
+      e = find_group(p.prefix, p.N, q);
+      const int p0 = p.prefix[e], nts = p.prefix[e + 1] - p0;
+      const int local = t - p0 * n_tiles;
+      n0 = local / nts * kTN;
+      m0 = (local % nts) * TM;
+      row0 = p.off[e];
+      m_end = p.off[e + 1] - row0;
+      kn = W == kGroupedFwd ? p.K : p.O;
+    }
+    const T* A;
+    const T* B;
+    int64_t lda, ldb;
+    if constexpr (W == kGroupedFwd) {
+      A = p.a + static_cast<int64_t>(row0) * p.K, lda = p.K;
+      B = p.b + static_cast<int64_t>(e) * p.O * p.K, ldb = p.K;
+    } else if constexpr (W == kGroupedDx) {
+      A = p.a + static_cast<int64_t>(row0) * p.O, lda = p.O;
+      B = p.b + static_cast<int64_t>(e) * p.O * p.K, ldb = p.K;
+    } else {
+      A = p.a + static_cast<int64_t>(row0) * p.O, lda = p.O;
+      B = p.b + static_cast<int64_t>(row0) * p.K, ldb = p.K;
+    }
+    // A value (index i of the tile dimension, k) per load; consecutive threads take
+    // consecutive addresses
+    constexpr int LA = TM * kTK / kSimtThreads, LB = kTN * kTK / kSimtThreads;
+    float ra[LA], rb[LB];
+    auto load = [&](int k0) {
+#pragma unroll
+      for (int j = 0; j < LA; ++j) {
+        const int x = tid + j * kSimtThreads;
+        const int i = kAk ? x / kTK : x % TM, k = kAk ? x % kTK : x / TM;
+        ra[j] = (m0 + i < m_end && k0 + k < kn)
+                    ? static_cast<float>(kAk ? A[(m0 + i) * lda + k0 + k] : A[(k0 + k) * lda + m0 + i])
+                    : 0.f;
+      }
+#pragma unroll
+      for (int j = 0; j < LB; ++j) {
+        const int x = tid + j * kSimtThreads;
+        const int i = kBk ? x / kTK : x % kTN, k = kBk ? x % kTK : x / kTN;
+        rb[j] = (n0 + i < n_cols && k0 + k < kn)
+                    ? static_cast<float>(kBk ? B[(n0 + i) * ldb + k0 + k] : B[(k0 + k) * ldb + n0 + i])
+                    : 0.f;
+      }
+    };
+    auto store = [&](int s) {
+#pragma unroll
+      for (int j = 0; j < LA; ++j) {
+        const int x = tid + j * kSimtThreads;
+        sA[s][kAk ? x % kTK : x / TM][kAk ? x / kTK : x % TM] = ra[j];
+      }
+#pragma unroll
+      for (int j = 0; j < LB; ++j) {
+        const int x = tid + j * kSimtThreads;
+        sB[s][kBk ? x % kTK : x / kTN][kBk ? x / kTK : x % kTN] = rb[j];
+      }
+    };
+    float c[RM][8];
+#pragma unroll
+    for (int i = 0; i < RM; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) c[i][j] = 0.f;
+    if (kn > 0) {
+      load(0);
+      store(0);
+    }
+    __syncthreads();
+    int s = 0;
+    for (int k0 = 0; k0 < kn; k0 += kTK) {
+      const bool more = k0 + kTK < kn;
+      if (more) load(k0 + kTK);
+#pragma unroll
+      for (int k = 0; k < kTK; ++k) {
+        float a[RM], b[8];
+        // columns 4 tx and 64 + 4 tx on: a quarter-warp reads consecutive 16-byte words
+        *reinterpret_cast<float4*>(b) = *reinterpret_cast<const float4*>(&sB[s][k][tx * 4]);
+        *reinterpret_cast<float4*>(b + 4) = *reinterpret_cast<const float4*>(&sB[s][k][64 + tx * 4]);
+        if constexpr (RM == 8) {
+          *reinterpret_cast<float4*>(a) = *reinterpret_cast<const float4*>(&sA[s][k][ty * 8]);
+          *reinterpret_cast<float4*>(a + 4) = *reinterpret_cast<const float4*>(&sA[s][k][ty * 8 + 4]);
+        } else {
+          *reinterpret_cast<float2*>(a) = *reinterpret_cast<const float2*>(&sA[s][k][ty * 2]);
+        }
+#pragma unroll
+        for (int i = 0; i < RM; ++i)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) c[i][j] = fmaf(a[i], b[j], c[i][j]);
+      }
+      if (more) store(s ^ 1);
+      __syncthreads();
+      s ^= 1;
+    }
+#pragma unroll
+    for (int i = 0; i < RM; ++i) {
+      const int m = m0 + ty * RM + i;
+      if (m >= m_end) continue;
+      T* o = W == kGroupedDw ? p.out + (static_cast<int64_t>(e) * p.O + m) * p.K
+                                 : p.out + (static_cast<int64_t>(row0) + m) * n_cols;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int n = n0 + (j < 4 ? tx * 4 + j : 64 + tx * 4 + j - 4);
+        if (n >= n_cols) continue;
+        float v = c[i][j];
+        if (W == kGroupedFwd && p.bias) v += static_cast<float>(p.bias[static_cast<int64_t>(e) * p.O + n]);
+        o[n] = static_cast<T>(v);
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------- bias gradient
+// One CTA per group and 32 columns: 8 interleaved runs of rows, then the runs in order.
+template <typename T>
+__global__ void __launch_bounds__(256)
+grouped_bias_grad_kernel(const T* __restrict__ dy, const int* __restrict__ off, T* __restrict__ db,
+                         const WsHeader* hdr, int O) {
+  __shared__ float buf[8][33];
+  pdl_trigger();
+  pdl_wait();
+  if (hdr->err) return;
+  const int e = blockIdx.x, lane = threadIdx.x & 31, k = threadIdx.x >> 5;
+  const int c = blockIdx.y * 32 + lane;
+  const int r1 = off[e + 1];
+  float v = 0.f;
+  if (c < O)
+#pragma unroll 4
+    for (int r = off[e] + k; r < r1; r += 8) v += static_cast<float>(dy[static_cast<int64_t>(r) * O + c]);
+  buf[k][lane] = v;
+  __syncthreads();
+  if (k == 0 && c < O) {
+    v = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v += buf[i][lane];
+    db[static_cast<int64_t>(e) * O + c] = static_cast<T>(v);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_grouped_plan(const GroupedShape& s, const GroupedPlan& p, const int* offsets,
+                                int tile_rows, cudaStream_t stream) {
+  count_launch();
+  return launch_dependent(grouped_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, offsets,
+                          p.tile_prefix, p.hdr, static_cast<int>(s.N), static_cast<int>(s.R),
+                          tile_rows);
+}
+
+// The narrow tile when a group has at most 40 rows on average: a full tile's
+// missing rows then cost more than the narrow tile's smaller reuse.
+int grouped_simt_tile_rows(const GroupedShape& s) { return s.R > 40 * s.N ? 128 : 32; }
+
+template <typename T>
+static cudaError_t launch_simt(const GroupedShape& s, const GroupedPlan& p, GroupedWhich which,
+                               const int* offsets, const void* a, const void* b, const void* bias,
+                               void* out, int num_sms, cudaStream_t stream) {
+  const SimtArgs<T> args = {static_cast<const T*>(a), static_cast<const T*>(b),
+                            static_cast<const T*>(bias), static_cast<T*>(out), offsets,
+                            p.tile_prefix, p.hdr, static_cast<int>(s.K), static_cast<int>(s.O),
+                            static_cast<int>(s.N)};
+  const int tm = which == kGroupedDw ? 128 : grouped_simt_tile_rows(s);
+  const int64_t cols = which == kGroupedFwd ? s.O : s.K;
+  const int64_t col_tiles = (cols + kTN - 1) / kTN;
+  const int64_t tiles = which == kGroupedDw ? s.N * ((s.O + 127) / 128) * col_tiles
+                                            : (s.R / tm + s.N) * col_tiles;   // at most
+  const int64_t most = static_cast<int64_t>(num_sms) * (tm == 128 ? 2 : 3);
+  const dim3 grid(static_cast<unsigned>(tiles < most ? tiles : most));
+  auto* kernel = which == kGroupedDw   ? grouped_simt_kernel<T, kGroupedDw, 128>
+                 : which == kGroupedDx ? (tm == 128 ? grouped_simt_kernel<T, kGroupedDx, 128>
+                                                    : grouped_simt_kernel<T, kGroupedDx, 32>)
+                                       : (tm == 128 ? grouped_simt_kernel<T, kGroupedFwd, 128>
+                                                    : grouped_simt_kernel<T, kGroupedFwd, 32>);
+  count_launch();
+  return launch_dependent(kernel, grid, dim3(kSimtThreads), 0, stream, args);
+}
+
+cudaError_t launch_grouped_simt(const GroupedShape& s, const GroupedPlan& p, GroupedWhich which,
+                                const int* offsets, const void* a, const void* b,
+                                const void* bias, void* out, int num_sms, cudaStream_t stream) {
+  return s.dtype == SWL_BF16
+             ? launch_simt<__nv_bfloat16>(s, p, which, offsets, a, b, bias, out, num_sms, stream)
+             : launch_simt<float>(s, p, which, offsets, a, b, bias, out, num_sms, stream);
+}
+
+cudaError_t launch_grouped_bias_grad(const GroupedShape& s, const GroupedPlan& p,
+                                     const int* offsets, const void* dy, void* db,
+                                     cudaStream_t stream) {
+  const dim3 grid(static_cast<unsigned>(s.N), static_cast<unsigned>((s.O + 31) / 32));
+  count_launch();
+  if (s.dtype == SWL_BF16)
+    return launch_dependent(grouped_bias_grad_kernel<__nv_bfloat16>, grid, dim3(256), 0, stream,
+                            static_cast<const __nv_bfloat16*>(dy), offsets,
+                            static_cast<__nv_bfloat16*>(db), p.hdr, static_cast<int>(s.O));
+  return launch_dependent(grouped_bias_grad_kernel<float>, grid, dim3(256), 0, stream,
+                          static_cast<const float*>(dy), offsets, static_cast<float*>(db), p.hdr,
+                          static_cast<int>(s.O));
+}
+
+namespace {
+
+bool aligned_to(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+swl_status grouped_shape(int64_t R, int64_t K, int64_t O, int64_t N, int dtype, GroupedShape* s) {
+  if (R < 0 || K <= 0 || O <= 0 || N <= 0) return SWL_ERR_INVALID_ARG;
+  if (dtype != SWL_F32 && dtype != SWL_BF16) return SWL_ERR_INVALID_ARG;
+  if (dtype == SWL_BF16 && (K % 8 != 0 || O % 8 != 0)) return SWL_ERR_UNSUPPORTED;
+  const int64_t lim = INT32_MAX;
+  if (N > kMaxExperts || R > lim / 2 || K > lim / 2 || O > lim / 2) return SWL_ERR_UNSUPPORTED;
+  if (N * (K > O ? K : O) > lim) return SWL_ERR_UNSUPPORTED;     // as the layer's weights
+  // work items of a launch fit an int
+  const int64_t wide = ((K > O ? K : O) + 31) / 32;
+  if ((R / 32 + N) * wide > lim || N * ((O + 31) / 32) * ((K + 31) / 32) > lim)
+    return SWL_ERR_UNSUPPORTED;
+  if ((O + 31) / 32 > 65535) return SWL_ERR_UNSUPPORTED;
+  *s = {R, K, O, N, dtype};
+  return SWL_OK;
+}
+
+size_t grouped_layout(const GroupedShape& s, uintptr_t base, GroupedPlan* p) {
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t o = at;
+    at += (bytes + 255) / 256 * 256;
+    return base + o;
+  };
+  GroupedPlan q;
+  q.hdr = reinterpret_cast<WsHeader*>(take(sizeof(WsHeader)));
+  q.tile_prefix = reinterpret_cast<int*>(take((static_cast<size_t>(s.N) + 1) * 4));
+  if (p) *p = q;
+  return at;
+}
+
+int grouped_sms() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+  return n;
+}
+
+struct GroupedSpan {
+  const void* p;
+  int64_t n;      // bytes
+};
+bool grouped_meet(const GroupedSpan& a, const GroupedSpan& b) {
+  if (!a.p || !b.p || !a.n || !b.n) return false;
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+  return x < y + b.n && y < x + a.n;
+}
+// Written ranges share a byte with one another or with a read one?
+bool grouped_clash(std::initializer_list<GroupedSpan> written,
+                   std::initializer_list<GroupedSpan> read) {
+  for (const GroupedSpan* a = written.begin(); a != written.end(); ++a) {
+    for (const GroupedSpan* b = written.begin(); b != a; ++b)
+      if (grouped_meet(*a, *b)) return true;
+    for (const GroupedSpan& r : read)
+      if (grouped_meet(*a, r)) return true;
+  }
+  return false;
+}
+
+}  // namespace
+}  // namespace swl
+
+using namespace swl;
+
+extern "C" swl_status switch_layer_grouped_workspace_size(int64_t R, int64_t K, int64_t O,
+                                                          int64_t N, int dtype, size_t* bytes) {
+  if (!bytes) return SWL_ERR_INVALID_ARG;
+  GroupedShape s;
+  const swl_status st = grouped_shape(R, K, O, N, dtype, &s);
+  if (st == SWL_OK) *bytes = grouped_layout(s, 0, nullptr);
+  return st;
+}
+
+extern "C" swl_status switch_layer_grouped_matmul(int64_t R, int64_t K, int64_t O, int64_t N,
+                                                  int dtype, const void* x,
+                                                  const int32_t* offsets, const void* W,
+                                                  const void* bias, void* y, void* workspace,
+                                                  size_t workspace_bytes, void* stream) {
+  GroupedShape s;
+  swl_status st = grouped_shape(R, K, O, N, dtype, &s);
+  if (st != SWL_OK) return st;
+  if (!offsets || !W || !workspace || (R > 0 && (!x || !y))) return SWL_ERR_INVALID_ARG;
+  const int64_t e = dtype == SWL_BF16 ? 2 : 4;
+  const uintptr_t al = dtype == SWL_BF16 ? 16 : 4;
+  if (!aligned_to(x, al) || !aligned_to(W, al) || !aligned_to(y, al) || !aligned_to(bias, dtype == SWL_BF16 ? 2 : 4) ||
+      !aligned_to(offsets, 4) || !aligned_to(workspace, 256))
+    return SWL_ERR_UNSUPPORTED;
+  GroupedPlan p;
+  const size_t need = grouped_layout(s, reinterpret_cast<uintptr_t>(workspace), &p);
+  if (workspace_bytes < need) return SWL_ERR_WORKSPACE;
+  if (grouped_clash({{y, R * O * e}, {workspace, static_cast<int64_t>(need)}},
+                    {{x, R * K * e}, {W, N * O * K * e}, {bias, N * O * e}, {offsets, (N + 1) * 4}}))
+    return SWL_ERR_INVALID_ARG;
+  const int sms = grouped_sms();
+  if (sms <= 0) return SWL_ERR_CUDA;
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  if (launch_grouped_plan(s, p, offsets, grouped_simt_tile_rows(s), cs) != cudaSuccess)
+    return SWL_ERR_CUDA;
+  if (R == 0) return SWL_OK;
+  if (launch_grouped_simt(s, p, kGroupedFwd, offsets, x, W, bias, y, sms, cs) != cudaSuccess)
+    return SWL_ERR_CUDA;
+  return SWL_OK;
+}
+
+extern "C" swl_status switch_layer_grouped_matmul_backward(
+    int64_t R, int64_t K, int64_t O, int64_t N, int dtype, const void* dy, const void* x,
+    const int32_t* offsets, const void* W, void* dx, void* dW, void* db, void* workspace,
+    size_t workspace_bytes, void* stream) {
+  GroupedShape s;
+  swl_status st = grouped_shape(R, K, O, N, dtype, &s);
+  if (st != SWL_OK) return st;
+  if (!offsets || !workspace || (R > 0 && (!dy || (dW && !x) || (dx && !W))) ||
+      (!dx && !dW && !db && R > 0))
+    return SWL_ERR_INVALID_ARG;
+  const int64_t e = dtype == SWL_BF16 ? 2 : 4;
+  const uintptr_t al = dtype == SWL_BF16 ? 16 : 4;
+  if (!aligned_to(dy, al) || !aligned_to(x, al) || !aligned_to(W, al) || !aligned_to(dx, al) ||
+      !aligned_to(dW, al) || !aligned_to(db, dtype == SWL_BF16 ? 2 : 4) || !aligned_to(offsets, 4) ||
+      !aligned_to(workspace, 256))
+    return SWL_ERR_UNSUPPORTED;
+  GroupedPlan p;
+  const size_t need = grouped_layout(s, reinterpret_cast<uintptr_t>(workspace), &p);
+  if (workspace_bytes < need) return SWL_ERR_WORKSPACE;
+  if (grouped_clash({{dx, R * K * e},
+                     {dW, N * O * K * e},
+                     {db, N * O * e},
+                     {workspace, static_cast<int64_t>(need)}},
+                    {{dy, R * O * e},
+                     {x, dW ? R * K * e : 0},
+                     {W, dx ? N * O * K * e : 0},
+                     {offsets, (N + 1) * 4}}))
+    return SWL_ERR_INVALID_ARG;
+  const int sms = grouped_sms();
+  if (sms <= 0) return SWL_ERR_CUDA;
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  if (launch_grouped_plan(s, p, offsets, grouped_simt_tile_rows(s), cs) != cudaSuccess)
+    return SWL_ERR_CUDA;
+  if (dx && R > 0 &&
+      launch_grouped_simt(s, p, kGroupedDx, offsets, dy, W, nullptr, dx, sms, cs) != cudaSuccess)
+    return SWL_ERR_CUDA;
+  if (dW &&
+      launch_grouped_simt(s, p, kGroupedDw, offsets, dy, x, nullptr, dW, sms, cs) != cudaSuccess)
+    return SWL_ERR_CUDA;
+  if (db && launch_grouped_bias_grad(s, p, offsets, dy, db, cs) != cudaSuccess) return SWL_ERR_CUDA;
+  return SWL_OK;
+}

@@ -1,0 +1,45 @@
+// Internal interface of the grouped products: the plan that the device makes
+// from the group offsets, and the launchers of the kernels that run on it.
+#pragma once
+
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "kernels.h"
+
+namespace swl {
+
+// One call's sizes: rows of the buffers, width of x, width of y, groups.
+struct GroupedShape {
+  int64_t R, K, O, N;
+  int dtype;
+};
+
+// Workspace of a call (device).
+struct GroupedPlan {
+  WsHeader* hdr;       // err, next_tile
+  int* tile_prefix;    // [N + 1] row tiles of groups before e (tile_rows rows each)
+};
+
+enum GroupedWhich : int { kGroupedFwd = 0, kGroupedDx = 1, kGroupedDw = 2 };
+
+// Reads and checks the offsets (0 <= off[0] <= ... <= off[N] <= R), counts the row
+// tiles and resets the header.  Bad offsets: kDevIndexOutOfRange and no tiles, so
+// that the kernels behind it touch nothing.
+cudaError_t launch_grouped_plan(const GroupedShape& s, const GroupedPlan& p, const int* offsets,
+                                int tile_rows, cudaStream_t stream);
+
+// Products on the CUDA cores in fp32.  which: y = x W^T + b
+// (kGroupedFwd: a = x, b = W, bias), dx = dy W (kGroupedDx: a = dy, b = W) or
+// dW = dy^T x (kGroupedDw: a = dy, b = x; every group written, empty ones zero).
+int grouped_simt_tile_rows(const GroupedShape& s);
+cudaError_t launch_grouped_simt(const GroupedShape& s, const GroupedPlan& p, GroupedWhich which,
+                                const int* offsets, const void* a, const void* b,
+                                const void* bias, void* out, int num_sms, cudaStream_t stream);
+
+// db[e] = sum of the group's rows of dy (fp32 sums in a fixed order).
+cudaError_t launch_grouped_bias_grad(const GroupedShape& s, const GroupedPlan& p,
+                                     const int* offsets, const void* dy, void* db,
+                                     cudaStream_t stream);
+
+}  // namespace swl

@@ -147,3 +147,59 @@ def test_norm_residual_backward_refusals(L):
     assert size(10, 64, 1, ctypes.byref(n)) == OK and n.value == 10 * 5 * 64 * 4
     assert size(1 << 30, 64, 1, ctypes.byref(n)) == OK and n.value < 1 << 20
     assert size(10, 64, 1, None) == INVALID and size(10, 1 << 20, 0, ctypes.byref(n)) == UNSUPPORTED
+
+
+# ---------------------------------------------------------------- grouped products
+def _grouped(L, R=100, K=64, O=128, N=4, dtype=swl.SWL_BF16, change=None, ws_bytes=1 << 20):
+    a = dict(x=0x100000, off=0x200000, W=0x300000, bias=0x400000, y=0x500000, ws=0x600000)
+    a.update(change or {})
+    before = L.switch_layer_launch_count()
+    st = L.switch_layer_grouped_matmul(R, K, O, N, dtype, a["x"], a["off"], a["W"], a["bias"],
+                                       a["y"], a["ws"], ws_bytes, None)
+    assert L.switch_layer_launch_count() == before
+    return st
+
+
+def _grouped_bwd(L, R=100, K=64, O=128, N=4, dtype=swl.SWL_BF16, change=None, ws_bytes=1 << 20):
+    a = dict(dy=0x080000, x=0x100000, off=0x200000, W=0x300000, dx=0x400000, dW=0x500000,
+             db=0x600000, ws=0x700000)
+    a.update(change or {})
+    before = L.switch_layer_launch_count()
+    st = L.switch_layer_grouped_matmul_backward(R, K, O, N, dtype, a["dy"], a["x"], a["off"],
+                                                a["W"], a["dx"], a["dW"], a["db"], a["ws"],
+                                                ws_bytes, None)
+    assert L.switch_layer_launch_count() == before
+    return st
+
+
+@pytest.mark.parametrize("call", [_grouped, _grouped_bwd], ids=["forward", "backward"])
+def test_grouped_refusals(L, call):
+    for kw in (dict(R=-1), dict(K=0), dict(O=0), dict(N=0), dict(dtype=3),
+               dict(change=dict(x=None)), dict(change=dict(off=None)), dict(change=dict(W=None)),
+               dict(change=dict(ws=None))):
+        assert call(L, **kw) == INVALID, kw
+    for kw in (dict(K=12), dict(O=20), dict(N=1 << 21), dict(R=1 << 31), dict(N=1 << 18, K=1 << 14),
+               dict(change=dict(x=0x100008)), dict(change=dict(W=0x300002)),
+               dict(change=dict(off=0x200002)), dict(change=dict(ws=0x600080)),
+               dict(dtype=swl.SWL_F32, change=dict(x=0x100002)), dict(R=1 << 29, K=1 << 13, O=8)):
+        assert call(L, **kw) == UNSUPPORTED, kw
+    assert call(L, ws_bytes=256) == WORKSPACE
+
+
+def test_grouped_refuses_overlaps(L):
+    for change in (dict(y=0x100000), dict(y=0x300100), dict(y=0x400010 - 0x10), dict(ws=0x500100),
+                   dict(y=0x200000), dict(y=None)):
+        assert _grouped(L, change=change) == INVALID, change
+    for change in (dict(dx=0x080000), dict(dx=0x100000), dict(dW=0x300000), dict(dx=0x500000),
+                   dict(db=0x500002), dict(ws=0x400000), dict(dy=None),
+                   dict(dx=None, dW=None, db=None)):
+        assert _grouped_bwd(L, change=change) == INVALID, change
+
+
+def test_grouped_workspace_size(L):
+    n = swl.switch_layer_grouped_workspace_size(1000, 64, 128, 2048, swl.SWL_BF16)
+    assert n >= 2049 * 4 + 256
+    with pytest.raises(swl.SwitchLayerError) as e:
+        swl.switch_layer_grouped_workspace_size(10, 12, 128, 4, swl.SWL_BF16)
+    assert e.value.status == UNSUPPORTED
+    assert L.switch_layer_grouped_workspace_size(10, 8, 8, 4, 1, None) == INVALID
