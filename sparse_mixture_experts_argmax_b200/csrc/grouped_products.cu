@@ -317,9 +317,7 @@ static cudaError_t launch_simt(const GroupedShape& s, const GroupedPlan& p, Grou
 cudaError_t launch_grouped_simt(const GroupedShape& s, const GroupedPlan& p, GroupedWhich which,
                                 const int* offsets, const void* a, const void* b,
                                 const void* bias, void* out, int num_sms, cudaStream_t stream) {
-  return s.dtype == SWL_BF16
-             ? launch_simt<__nv_bfloat16>(s, p, which, offsets, a, b, bias, out, num_sms, stream)
-             : launch_simt<float>(s, p, which, offsets, a, b, bias, out, num_sms, stream);
+  return launch_simt<float>(s, p, which, offsets, a, b, bias, out, num_sms, stream);
 }
 
 cudaError_t launch_grouped_bias_grad(const GroupedShape& s, const GroupedPlan& p,
@@ -366,6 +364,8 @@ size_t grouped_layout(const GroupedShape& s, uintptr_t base, GroupedPlan* p) {
   GroupedPlan q;
   q.hdr = reinterpret_cast<WsHeader*>(take(sizeof(WsHeader)));
   q.tile_prefix = reinterpret_cast<int*>(take((static_cast<size_t>(s.N) + 1) * 4));
+  q.maps = reinterpret_cast<void*>(
+      take(s.dtype == SWL_BF16 ? static_cast<size_t>(s.N) * 2 * sizeof(CUtensorMap) : 0));
   if (p) *p = q;
   return at;
 }
@@ -375,6 +375,16 @@ int grouped_sms() {
   if (cudaGetDevice(&dev) != cudaSuccess) return 0;
   if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
   return n;
+}
+
+int tile_rows(const GroupedShape& s) {
+  return s.dtype == SWL_BF16 ? grouped_sm100_tile_rows(s) : grouped_simt_tile_rows(s);
+}
+cudaError_t launch_product(const GroupedShape& s, const GroupedPlan& p, GroupedWhich which,
+                           const int* offsets, const void* a, const void* b, const void* bias,
+                           void* out, int sms, cudaStream_t stream) {
+  return (s.dtype == SWL_BF16 ? launch_grouped_sm100 : launch_grouped_simt)(
+      s, p, which, offsets, a, b, bias, out, sms, stream);
 }
 
 struct GroupedSpan {
@@ -435,10 +445,10 @@ extern "C" swl_status switch_layer_grouped_matmul(int64_t R, int64_t K, int64_t 
   const int sms = grouped_sms();
   if (sms <= 0) return SWL_ERR_CUDA;
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
-  if (launch_grouped_plan(s, p, offsets, grouped_simt_tile_rows(s), cs) != cudaSuccess)
+  if (launch_grouped_plan(s, p, offsets, tile_rows(s), cs) != cudaSuccess)
     return SWL_ERR_CUDA;
   if (R == 0) return SWL_OK;
-  if (launch_grouped_simt(s, p, kGroupedFwd, offsets, x, W, bias, y, sms, cs) != cudaSuccess)
+  if (launch_product(s, p, kGroupedFwd, offsets, x, W, bias, y, sms, cs) != cudaSuccess)
     return SWL_ERR_CUDA;
   return SWL_OK;
 }
@@ -474,13 +484,13 @@ extern "C" swl_status switch_layer_grouped_matmul_backward(
   const int sms = grouped_sms();
   if (sms <= 0) return SWL_ERR_CUDA;
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
-  if (launch_grouped_plan(s, p, offsets, grouped_simt_tile_rows(s), cs) != cudaSuccess)
+  if (launch_grouped_plan(s, p, offsets, tile_rows(s), cs) != cudaSuccess)
     return SWL_ERR_CUDA;
   if (dx && R > 0 &&
-      launch_grouped_simt(s, p, kGroupedDx, offsets, dy, W, nullptr, dx, sms, cs) != cudaSuccess)
+      launch_product(s, p, kGroupedDx, offsets, dy, W, nullptr, dx, sms, cs) != cudaSuccess)
     return SWL_ERR_CUDA;
   if (dW &&
-      launch_grouped_simt(s, p, kGroupedDw, offsets, dy, x, nullptr, dW, sms, cs) != cudaSuccess)
+      launch_product(s, p, kGroupedDw, offsets, dy, x, nullptr, dW, sms, cs) != cudaSuccess)
     return SWL_ERR_CUDA;
   if (db && launch_grouped_bias_grad(s, p, offsets, dy, db, cs) != cudaSuccess) return SWL_ERR_CUDA;
   return SWL_OK;

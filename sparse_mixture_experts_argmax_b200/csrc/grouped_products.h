@@ -19,6 +19,7 @@ struct GroupedShape {
 struct GroupedPlan {
   WsHeader* hdr;       // err, next_tile
   int* tile_prefix;    // [N + 1] row tiles of groups before e (tile_rows rows each)
+  void* maps;          // bf16: [2 N] tensor maps, dy's and x's rows up to each group's end
 };
 
 enum GroupedWhich : int { kGroupedFwd = 0, kGroupedDx = 1, kGroupedDw = 2 };
@@ -36,6 +37,12 @@ int grouped_simt_tile_rows(const GroupedShape& s);
 cudaError_t launch_grouped_simt(const GroupedShape& s, const GroupedPlan& p, GroupedWhich which,
                                 const int* offsets, const void* a, const void* b,
                                 const void* bias, void* out, int num_sms, cudaStream_t stream);
+
+// The same on the tensor cores (bf16 tensors), two launches for dW.
+int grouped_sm100_tile_rows(const GroupedShape& s);
+cudaError_t launch_grouped_sm100(const GroupedShape& s, const GroupedPlan& p, GroupedWhich which,
+                                 const int* offsets, const void* a, const void* b,
+                                 const void* bias, void* out, int num_sms, cudaStream_t stream);
 
 // db[e] = sum of the group's rows of dy (fp32 sums in a fixed order).
 cudaError_t launch_grouped_bias_grad(const GroupedShape& s, const GroupedPlan& p,

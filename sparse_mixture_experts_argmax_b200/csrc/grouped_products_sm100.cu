@@ -1,0 +1,608 @@
+// Products grouped by expert on the 5th-generation tensor cores, bf16 with fp32
+// accumulation in TMEM: y = x W^T + b, dx = dy W and dW = dy^T x over ragged
+// row ranges, one persistent kernel for each.
+//
+// A pair of CTAs (a cluster of two, cta_group::2) computes D[256, n], n <= 256:
+// each CTA holds 128 of the 256 rows of A and n / 2 of the n rows of B, so a
+// 64-deep step of a full tile brings 32 KB into each SM for 512 cycles of
+// tensor work; a single CTA's 128 x 256 tile would need 48 KB, more than the L2
+// delivers.  D lies in TMEM, lane = row of A, column = row of B:
+//   y, dx:  A = 256 features of W[e], B = the tile's token rows.  The ragged side is
+//           n, which follows the rows that are there in steps of 32 (64 for tiles of
+//           over 64 rows): a group of a few rows reads W once and multiplies little.
+//   dW:     A = 256 columns of dy, B = 256 columns of x, summed over the group's rows.
+//           The tensor maps of dy and x end at the group's last row (the plan writes a
+//           pair of maps per group): the hardware fills the rows behind it with zeros,
+//           whatever the next group holds there.
+// An operand whose contiguous axis is the summed one is K-major (W and x for y,
+// dy for dx); one whose summed axis is the slow one is MN-major (W for dx; dy and x
+// for dW).  Both come by TMA in 128-byte-swizzled boxes 64 elements wide; no operand
+// is transposed in memory.
+//
+// Roles of a CTA's 12 warps: 0 TMA producer, 1 MMA issuer (first CTA of the pair
+// only), 2 TMEM, 3 tile decoder, 4-11 epilogue (two warps per lane quarter).  Two
+// 256-column accumulators, so a tile's epilogue runs under the next tile's products.
+// Tiles go round the pairs in order; the row tiles of a group are consecutive.
+// Every wait is bounded: one that runs out sets the device error word and the CTA
+// drains and leaves.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "grouped_products.h"
+#include "sm100_ptx.cuh"
+
+namespace swl {
+namespace {
+
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = 128 + 32 * kEpiWarps;
+constexpr int kBK = 64;                          // depth of a stage (128 bytes of bf16)
+constexpr uint32_t kABytes = 128 * kBK * 2;      // a CTA's half of A
+constexpr int kMaxStages = 12;
+constexpr int kAccs = 2;
+constexpr int kTmemCols = 512;
+constexpr int kTileRing = 8;
+constexpr int kEpiBytes = kEpiWarps * 32 * 32 * 2;
+constexpr size_t kSmemLimit = 227 * 1024;
+
+struct Args {
+  const int* off;
+  const int* prefix;
+  WsHeader* hdr;
+  const CUtensorMap* maps;      // dW: [2 N] maps of dy and x per group
+  const __nv_bfloat16* bias;
+  __nv_bfloat16* out;
+  unsigned long long wait_ns;
+  int N;
+  int m;           // rows of D per group: O (y, dW) or K (dx); the epilogue's features
+  int cols;        // dW: columns of D (K)
+  int k_blocks;    // y, dx: ceil(depth / 64)
+  int m_tiles, n_tiles;   // n_tiles: dW only
+  int bn;          // most rows of B per tile
+  int box;         // y, dx: rows per TMA box of B
+  int stages;
+  int keep_w;      // W is read by several row tiles: no evict-first
+};
+
+struct Tile {
+  int t;           // -1: no more
+  int e, m0, row0, rows, n, n0, kb;
+};
+
+// ---------------------------------------------------------------- pair PTX
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
+                   : "memory");
+}
+// Address of the first CTA's copy of a shared variable.
+__device__ __forceinline__ uint32_t leader_addr(const void* p) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(ptx::smem_u32(p)));
+  return a;
+}
+__device__ __forceinline__ void arrive_at(uint32_t cluster_bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar)
+               : "memory");
+}
+__device__ __forceinline__ void pair_tmem_alloc(uint32_t* dst, uint32_t cols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                   ptx::smem_u32(dst)),
+               "r"(cols)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void pair_tmem_dealloc(uint32_t addr, uint32_t cols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols)
+               : "memory");
+}
+__device__ __forceinline__ void pair_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                         uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Arrive on both CTAs' copies of `bar` once this thread's products have finished.
+__device__ __forceinline__ void pair_commit(uint64_t* bar) {
+  const uint16_t both = 3;
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
+      "[%0], %1;" ::"r"(ptx::smem_u32(bar)),
+      "h"(both)
+      : "memory");
+}
+// TMA loads into this CTA's shared memory that complete on the first CTA's barrier.
+__device__ __forceinline__ void pair_load_2d(void* dst, const CUtensorMap* map, uint32_t bar,
+                                             int c0, int c1, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      ".L2::cache_hint [%0], [%1, {%3, %4}], [%2], %5;" ::"r"(ptx::smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "l"(policy)
+      : "memory");
+}
+__device__ __forceinline__ void pair_load_3d(void* dst, const CUtensorMap* map, uint32_t bar,
+                                             int c0, int c1, int c2, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      ".L2::cache_hint [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(ptx::smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "l"(policy)
+      : "memory");
+}
+__device__ __forceinline__ uint64_t l2_policy_normal() {
+  uint64_t p;
+  asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
+// MN-major bf16 tile in 128-byte-swizzled boxes of [64 k][64 mn]: 8-row groups along
+// k 1024 bytes apart (stride offset), boxes along mn 8192 bytes apart (leading offset).
+__device__ __forceinline__ uint64_t desc_mn_major(uint32_t addr) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((addr >> 4) & 0x3FFFu);
+  d |= static_cast<uint64_t>(8192u >> 4) << 16;
+  d |= static_cast<uint64_t>(1024u >> 4) << 32;
+  d |= static_cast<uint64_t>(1u) << 46;
+  d |= static_cast<uint64_t>(2u) << 61;
+  return d;
+}
+template <bool kMn>
+__device__ __forceinline__ uint64_t operand_desc(uint32_t base, int k) {
+  // 16 deep: 32 bytes along a K-major row, or 16 rows of 128 bytes
+  return kMn ? desc_mn_major(base + k * 2048) : ptx::umma_desc_sw128_kmajor(base + k * 32);
+}
+
+// ---------------------------------------------------------------- the kernel
+template <int W>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+grouped_sm100_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                     const __grid_constant__ Args args) {
+  constexpr bool kAmn = W != kGroupedFwd, kBmn = W == kGroupedDw;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  const int stages = args.stages;
+  const uint32_t b_bytes = static_cast<uint32_t>(args.bn / 2) * kBK * 2;
+  uint8_t* smem_a = smem;
+  uint8_t* smem_b = smem_a + stages * kABytes;
+  __nv_bfloat16* epi = reinterpret_cast<__nv_bfloat16*>(smem_b + stages * b_bytes);
+  uint64_t* full = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(epi) + kEpiBytes);
+  uint64_t* empty = full + kMaxStages;
+  uint64_t* tfull = empty + kMaxStages;
+  uint64_t* tempty = tfull + kAccs;
+  uint64_t* drain = tempty + kAccs;
+  uint64_t* ring_full = drain + 1;
+  uint64_t* ring_empty = ring_full + kTileRing;
+  Tile* ring = reinterpret_cast<Tile*>(ring_empty + kTileRing);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(ring + kTileRing);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  const bool leader = rank == 0;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < stages; ++s) {
+      ptx::mbar_init(&full[s], 1);
+      ptx::mbar_init(&empty[s], 1);
+    }
+    for (int i = 0; i < kAccs; ++i) {
+      ptx::mbar_init(&tfull[i], 1);
+      ptx::mbar_init(&tempty[i], 2 * kEpiWarps);     // both CTAs' epilogue warps
+    }
+    ptx::mbar_init(drain, 1);
+    for (int i = 0; i < kTileRing; ++i) {
+      ptx::mbar_init(&ring_full[i], 1);
+      ptx::mbar_init(&ring_empty[i], kEpiWarps + 1 + (leader ? 1 : 0));
+    }
+    *abort_flag = 0;
+    ptx::fence_mbar_init();
+    ptx::fence_proxy_async_smem();
+    if (W != kGroupedDw) {
+      ptx::prefetch_tmap(&tmA);
+      ptx::prefetch_tmap(&tmB);
+    }
+  }
+  __syncthreads();
+  if (warp == 2) pair_tmem_alloc(tmem_slot, kTmemCols);
+  ptx::tc_fence_before();
+  cluster_sync();              // barriers and TMEM of both CTAs exist
+  ptx::tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  pdl_trigger();
+  pdl_wait();
+
+  const int total = W == kGroupedDw ? (args.hdr->err ? 0 : args.N * args.m_tiles * args.n_tiles)
+                                    : args.prefix[args.N] * args.m_tiles;
+  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  auto fail = [&]() {
+    *abort_flag = 1;
+    atomicExch(&args.hdr->err, static_cast<int>(kDevPipelineTimeout));
+  };
+
+  if (warp == 3) {
+    // ------------------------------------------------------------ tile decoder
+    if (lane == 0) {
+      int t = pair;
+      for (int i = 0;; ++i, t += pairs) {
+        const int slot = i % kTileRing;
+        if (!ptx::mbar_wait(&ring_empty[slot], ((i / kTileRing) & 1) ^ 1u, abort_flag, args.wait_ns)) {
+          fail();
+          break;
+        }
+        Tile ts = {};
+        ts.t = t < total ? t : -1;
+        if (ts.t >= 0) {
+          if constexpr (W == kGroupedDw) {
+            const int per = args.m_tiles * args.n_tiles;
+            ts.e = t / per;
+            const int r = t - ts.e * per;
+            ts.m0 = r / args.n_tiles * 256;
+            ts.n0 = (r % args.n_tiles) * 256;
+            ts.row0 = __ldg(args.off + ts.e);
+            ts.rows = __ldg(args.off + ts.e + 1) - ts.row0;
+            ts.n = min(256, (args.cols - ts.n0 + 127) & ~127);
+            ts.kb = (ts.rows + kBK - 1) / kBK;
+          } else {
+            const int q = t / args.m_tiles;
+            int lo = 0, hi = args.N;
+            while (hi - lo > 1) {
+              const int mid = (lo + hi) >> 1;
+              if (__ldg(args.prefix + mid) <= q) lo = mid;
+              else hi = mid;
+            }
+            const int p0 = __ldg(args.prefix + lo), nts = __ldg(args.prefix + lo + 1) - p0;
+            const int local = t - p0 * args.m_tiles;
+            const int nt = local % nts;
+            ts.e = lo;
+            ts.m0 = local / nts * 256;
+            const int begin = __ldg(args.off + lo), end = __ldg(args.off + lo + 1);
+            ts.row0 = begin + nt * args.bn;
+            ts.rows = min(args.bn, end - ts.row0);
+            const int step = 2 * args.box;
+            ts.n = (ts.rows + step - 1) / step * step;
+            ts.kb = args.k_blocks;
+          }
+        }
+        ring[slot] = ts;
+        ptx::mbar_arrive(&ring_full[slot]);
+        if (ts.t < 0) break;
+      }
+    }
+    __syncwarp();
+  } else if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    if (lane == 0) {
+      const uint64_t keep = ptx::l2_policy_evict_last();
+      const uint64_t norm = l2_policy_normal();
+      const uint64_t pol_a = W == kGroupedDw || args.keep_w ? norm : ptx::l2_policy_evict_first();
+      const uint64_t pol_b = W == kGroupedDw ? norm : keep;
+      int stage = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      for (int i = 0; ok; ++i) {
+        const int slot = i % kTileRing;
+        if (!ptx::mbar_wait(&ring_full[slot], (i / kTileRing) & 1, abort_flag, args.wait_ns)) {
+          fail();
+          ok = false;
+          break;
+        }
+        const Tile ts = ring[slot];
+        ptx::mbar_arrive(&ring_empty[slot]);
+        if (ts.t < 0) break;
+        const CUtensorMap* mapA = &tmA;
+        const CUtensorMap* mapB = &tmB;
+        if constexpr (W == kGroupedDw) {
+          mapA = args.maps + 2 * ts.e;
+          mapB = mapA + 1;
+          // the maps were written by another kernel's ordinary stores
+          asm volatile("fence.proxy.tensormap::generic.acquire.gpu [%0], 128;" ::"l"(mapA) : "memory");
+          asm volatile("fence.proxy.tensormap::generic.acquire.gpu [%0], 128;" ::"l"(mapB) : "memory");
+        }
+        const int half = ts.n >> 1;              // this CTA's rows of B
+        const int m0 = ts.m0 + static_cast<int>(rank) * 128;
+        const uint32_t bytes = 2 * (kABytes + static_cast<uint32_t>(half) * kBK * 2);
+        for (int kb = 0; kb < ts.kb; ++kb) {
+          if (!ptx::mbar_wait(&empty[stage], ph ^ 1u, abort_flag, args.wait_ns)) {
+            fail();
+            ok = false;
+            break;
+          }
+          if (leader) ptx::mbar_arrive_expect_tx(&full[stage], bytes);
+          const uint32_t bar = leader_addr(&full[stage]);
+          uint8_t* a = smem_a + stage * kABytes;
+          uint8_t* b = smem_b + stage * b_bytes;
+          if constexpr (W == kGroupedFwd) {
+            pair_load_3d(a, mapA, bar, kb * kBK, m0, ts.e, pol_a);
+          } else if constexpr (W == kGroupedDx) {
+            pair_load_3d(a, mapA, bar, m0, kb * kBK, ts.e, pol_a);
+            pair_load_3d(a + 8192, mapA, bar, m0 + 64, kb * kBK, ts.e, pol_a);
+          } else {
+            pair_load_2d(a, mapA, bar, m0, ts.row0 + kb * kBK, pol_a);
+            pair_load_2d(a + 8192, mapA, bar, m0 + 64, ts.row0 + kb * kBK, pol_a);
+          }
+          if constexpr (W == kGroupedDw) {
+            const int n0 = ts.n0 + static_cast<int>(rank) * half;
+            for (int j = 0; j < half; j += 64)
+              pair_load_2d(b + j * 128, mapB, bar, n0 + j, ts.row0 + kb * kBK, pol_b);
+          } else {
+            const int r0 = ts.row0 + static_cast<int>(rank) * half;
+            for (int j = 0; j < half; j += args.box)
+              pair_load_2d(b + j * 128, mapB, bar, kb * kBK, r0 + j, pol_b);
+          }
+          if (++stage == stages) {
+            stage = 0;
+            ph ^= 1u;
+          }
+        }
+      }
+      // after a failure: copies in flight (microseconds) land before the CTAs leave
+      if (!ok)
+        for (int i = 0; i < 1000; ++i) __nanosleep(1000);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer
+    if (leader && lane == 0) {
+      int stage = 0, acc = 0;
+      uint32_t ph = 0, aph = 0;
+      bool ok = true;
+      for (int i = 0; ok; ++i) {
+        const int slot = i % kTileRing;
+        if (!ptx::mbar_wait(&ring_full[slot], (i / kTileRing) & 1, abort_flag, args.wait_ns)) {
+          fail();
+          break;
+        }
+        const Tile ts = ring[slot];
+        ptx::mbar_arrive(&ring_empty[slot]);
+        if (ts.t < 0) break;
+        if (ts.kb == 0) continue;
+        if (!ptx::mbar_wait(&tempty[acc], aph ^ 1u, abort_flag, args.wait_ns)) {
+          fail();
+          break;
+        }
+        ptx::tc_fence_after();
+        const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | (kAmn ? 1u << 15 : 0u) |
+                               (kBmn ? 1u << 16 : 0u) | ((static_cast<uint32_t>(ts.n) >> 3) << 17) |
+                               ((256u >> 4) << 24);
+        const uint32_t d = tmem + static_cast<uint32_t>(acc * (kTmemCols / kAccs));
+        for (int kb = 0; kb < ts.kb; ++kb) {
+          if (!ptx::mbar_wait(&full[stage], ph, abort_flag, args.wait_ns)) {
+            fail();
+            ok = false;
+            break;
+          }
+          ptx::tc_fence_after();
+          const uint32_t a = ptx::smem_u32(smem_a + stage * kABytes);
+          const uint32_t b = ptx::smem_u32(smem_b + stage * b_bytes);
+#pragma unroll
+          for (int k = 0; k < kBK / 16; ++k)
+            pair_mma(d, operand_desc<kAmn>(a, k), operand_desc<kBmn>(b, k), idesc,
+                     kb != 0 || k != 0 ? 1u : 0u);
+          pair_commit(&empty[stage]);
+          if (++stage == stages) {
+            stage = 0;
+            ph ^= 1u;
+          }
+        }
+        if (!ok) break;
+        pair_commit(&tfull[acc]);
+        if (++acc == kAccs) {
+          acc = 0;
+          aph ^= 1u;
+        }
+      }
+      // every product has finished before the pair's memory is given back
+      asm volatile(
+          "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+              ptx::smem_u32(drain))
+          : "memory");
+      volatile int never = 0;
+      if (!ptx::mbar_wait(drain, 0u, &never, args.wait_ns)) fail();
+    }
+    __syncwarp();
+  } else if (warp >= 4) {
+    // ------------------------------------------------------------ epilogue
+    const int q = warp & 3, side = (warp - 4) >> 2;
+    __nv_bfloat16* st = epi + (warp - 4) * 32 * 32;      // [32 rows][32 features]
+    const uint32_t tempty0 = leader_addr(&tempty[0]), tempty1 = leader_addr(&tempty[1]);
+    int acc = 0;
+    uint32_t aph = 0;
+    for (int i = 0;; ++i) {
+      const int slot = i % kTileRing;
+      if (!__all_sync(0xffffffffu, ptx::mbar_wait(&ring_full[slot], (i / kTileRing) & 1, abort_flag,
+                                                  args.wait_ns))) {
+        fail();
+        break;
+      }
+      const Tile ts = ring[slot];
+      if (ts.t < 0) break;
+      const int f0 = ts.m0 + static_cast<int>(rank) * 128 + q * 32;   // this warp's rows of D
+      const int f = f0 + lane;
+      float bias = 0.f;
+      if (W == kGroupedFwd && args.bias != nullptr && f < args.m)
+        bias = __bfloat162float(args.bias[static_cast<size_t>(ts.e) * args.m + f]);
+      const uint32_t t0 = tmem + static_cast<uint32_t>(acc * (kTmemCols / kAccs)) +
+                          (static_cast<uint32_t>(q * 32) << 16);
+      if (ts.kb > 0) {
+        if (!__all_sync(0xffffffffu, ptx::mbar_wait(&tfull[acc], aph, abort_flag, args.wait_ns))) {
+          fail();
+          break;
+        }
+        ptx::tc_fence_after();
+      }
+      const int width = W == kGroupedDw ? min(ts.n, args.cols - ts.n0) : ts.rows;
+      for (int c0 = side * 32; c0 < width; c0 += 64) {
+        uint32_t r[32];
+        if (ts.kb > 0) {
+          ptx::tmem_ld_32x32b_x32(t0 + static_cast<uint32_t>(c0), r);
+          ptx::tmem_ld_wait();
+        } else {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) r[j] = 0u;
+        }
+        if constexpr (W == kGroupedDw) {
+          // a lane's 32 columns are consecutive in memory
+          if (f < args.m) {
+            __nv_bfloat16* o = args.out + (static_cast<size_t>(ts.e) * args.m + f) * args.cols + ts.n0 + c0;
+#pragma unroll
+            for (int j = 0; j < 32; j += 8) {
+              if (c0 + j >= width) break;       // cols % 8 == 0
+              __nv_bfloat162 v[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                v[k] = __floats2bfloat162_rn(__uint_as_float(r[j + 2 * k]), __uint_as_float(r[j + 2 * k + 1]));
+              *reinterpret_cast<uint4*>(o + j) = *reinterpret_cast<const uint4*>(v);
+            }
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 32; j += 2) {     // two rows per conversion
+            const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(r[j]) + bias,
+                                                           __uint_as_float(r[j + 1]) + bias);
+            st[j * 32 + lane] = h.x;
+            st[(j + 1) * 32 + lane] = h.y;
+          }
+          __syncwarp();
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int idx = lane + 32 * k;
+            const int j = idx >> 2, part = idx & 3;
+            if (c0 + j < ts.rows && f0 + part * 8 < args.m)
+              *reinterpret_cast<uint4*>(args.out + static_cast<size_t>(ts.row0 + c0 + j) * args.m +
+                                        f0 + part * 8) =
+                  *reinterpret_cast<const uint4*>(st + j * 32 + part * 8);
+          }
+          __syncwarp();
+        }
+      }
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (ts.kb > 0) arrive_at(acc == 0 ? tempty0 : tempty1);
+        ptx::mbar_arrive(&ring_empty[slot]);
+      }
+      if (ts.kb > 0 && ++acc == kAccs) {
+        acc = 0;
+        aph ^= 1u;
+      }
+    }
+  }
+  __syncwarp();
+  ptx::tc_fence_before();
+  cluster_sync();              // neither CTA leaves while the other may reach into it
+  if (warp == 2) {
+    ptx::tc_fence_after();
+    pair_tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// ---------------------------------------------------------------- dW's maps
+// One warp per group: the two template maps with the rows ended at offsets[e + 1].
+__global__ void __launch_bounds__(256)
+grouped_maps_kernel(const __grid_constant__ CUtensorMap dy, const __grid_constant__ CUtensorMap x,
+                    CUtensorMap* __restrict__ maps, const int* __restrict__ off,
+                    const WsHeader* hdr, int N) {
+  pdl_trigger();
+  pdl_wait();
+  const int e = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if (e >= N || hdr->err) return;
+  const int end = off[e + 1];
+  if (end <= off[e]) return;             // no rows: its maps are never read
+  CUtensorMap* m = maps + 2 * e;
+  if (lane < 16)
+    reinterpret_cast<uint4*>(m)[lane] =
+        reinterpret_cast<const uint4*>(lane < 8 ? &dy : &x)[lane & 7];
+  __syncwarp();
+  if (lane < 2) {
+    asm volatile("tensormap.replace.tile.global_dim.global.b1024.b32 [%0], 1, %1;" ::"l"(m + lane),
+                 "r"(end)
+                 : "memory");
+    asm volatile("fence.proxy.tensormap::generic.release.gpu;" ::: "memory");
+  }
+}
+
+}  // namespace
+
+// Rows of B per tile, at most: 256 once the groups have 48 rows on average (one pass
+// over W for most), fewer for few rows (more stages fit, and n follows the rows in
+// steps of 32 instead of 64).
+int grouped_sm100_tile_rows(const GroupedShape& s) { return s.R >= 48 * s.N ? 256 : 64; }
+
+cudaError_t launch_grouped_sm100(const GroupedShape& s, const GroupedPlan& p, GroupedWhich which,
+                                 const int* offsets, const void* a, const void* b,
+                                 const void* bias, void* out, int num_sms, cudaStream_t stream) {
+  const uint64_t K = s.K, O = s.O, N = s.N, R = s.R;
+  CUtensorMap mapA, mapB;
+  Args g = {};
+  g.off = offsets;
+  g.prefix = p.tile_prefix;
+  g.hdr = p.hdr;
+  g.maps = static_cast<const CUtensorMap*>(p.maps);
+  g.bias = static_cast<const __nv_bfloat16*>(bias);
+  g.out = static_cast<__nv_bfloat16*>(out);
+  g.wait_ns = wait_limit_ns();
+  g.N = static_cast<int>(N);
+  int64_t tiles;      // at most
+  if (which == kGroupedDw) {
+    const uint64_t da[2] = {O, R}, db[2] = {K, R};
+    const uint32_t box[2] = {64, 64};
+    // rows 0 (an empty batch): every group is empty, the maps are not made
+    if (R > 0) {
+      if (!encode_tmap_bf16(&mapA, a, 2, da, box) || !encode_tmap_bf16(&mapB, b, 2, db, box))
+        return cudaErrorInvalidValue;
+      count_launch();
+      const cudaError_t e =
+          launch_dependent(grouped_maps_kernel, dim3(static_cast<unsigned>((N + 7) / 8)), dim3(256),
+                           0, stream, mapA, mapB, static_cast<CUtensorMap*>(p.maps), offsets,
+                           p.hdr, g.N);
+      if (e != cudaSuccess) return e;
+    } else {
+      mapA = mapB = CUtensorMap{};
+    }
+    g.m = static_cast<int>(O);
+    g.cols = static_cast<int>(K);
+    g.n_tiles = static_cast<int>((K + 255) / 256);
+    g.bn = K <= 128 ? 128 : 256;
+    g.box = 64;
+    g.m_tiles = (g.m + 255) / 256;
+    tiles = static_cast<int64_t>(N) * g.m_tiles * g.n_tiles;
+  } else {
+    const uint64_t dw[3] = {K, O, N}, dr[2] = {which == kGroupedFwd ? K : O, R};
+    const uint32_t bw[3] = {64, which == kGroupedFwd ? 128u : 64u, 1};
+    g.bn = grouped_sm100_tile_rows(s);
+    g.box = g.bn > 64 ? 32 : 16;
+    const uint32_t br[2] = {64, static_cast<uint32_t>(g.box)};
+    // a is the row operand (x, dy), b is W
+    if (!encode_tmap_bf16(&mapA, b, 3, dw, bw) || !encode_tmap_bf16(&mapB, a, 2, dr, br))
+      return cudaErrorInvalidValue;
+    g.m = static_cast<int>(which == kGroupedFwd ? O : K);
+    g.k_blocks = static_cast<int>((dr[0] + kBK - 1) / kBK);
+    g.m_tiles = (g.m + 255) / 256;
+    g.keep_w = s.R > 2 * g.bn * s.N;
+    tiles = (s.R / g.bn + s.N) * g.m_tiles;
+  }
+  const size_t stage = kABytes + static_cast<size_t>(g.bn / 2) * kBK * 2;
+  const size_t fixed = 1024 + kEpiBytes + (2 * kMaxStages + 2 * kAccs + 1 + 2 * kTileRing) * 8 +
+                       kTileRing * sizeof(Tile) + 64;
+  int stages = static_cast<int>((kSmemLimit - fixed) / stage);
+  g.stages = stages < kMaxStages ? stages : kMaxStages;
+  const size_t smem = fixed + g.stages * stage;
+  auto* kernel = which == kGroupedFwd  ? grouped_sm100_kernel<kGroupedFwd>
+                 : which == kGroupedDx ? grouped_sm100_kernel<kGroupedDx>
+                                       : grouped_sm100_kernel<kGroupedDw>;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
+  const int64_t pairs = num_sms / 2;
+  count_launch();
+  return launch_dependent(kernel, dim3(static_cast<unsigned>(2 * (tiles < pairs ? tiles : pairs))),
+                          dim3(kThreads), smem, stream, mapA, mapB, g);
+}
+
+}  // namespace swl

@@ -287,6 +287,11 @@ int bf16_tile_rows(int64_t C_eff);
 inline int ffn_accumulators(int tile_rows) { return tile_rows <= 128 ? 4 : 2; }
 constexpr int kF32TileRows = 32;
 
+// Tensor map of a contiguous bf16 tensor (2 or 3 dimensions, innermost first), boxes
+// 64 elements wide with 128-byte swizzle (switch_layer.cu).
+bool encode_tmap_bf16(CUtensorMap* m, const void* ptr, int rank, const uint64_t* dims,
+                      const uint32_t* box);
+
 // Number of kernel launches issued by this library since load.
 void count_launch(int n = 1);
 // Bound of every wait inside the kernels, in ns (switch_layer_set_wait_limit_ns).

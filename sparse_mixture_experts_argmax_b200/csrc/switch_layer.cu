@@ -140,6 +140,25 @@ static bool make_tmap_bf16(CUtensorMap* m, const void* ptr, uint64_t inner, uint
   return r == CUDA_SUCCESS;
 }
 
+// Contiguous bf16 tensor of `rank` (2 or 3) dimensions, innermost first, 128-byte
+// swizzled boxes 64 elements wide.
+bool encode_tmap_bf16(CUtensorMap* m, const void* ptr, int rank, const uint64_t* dims,
+                      const uint32_t* box) {
+  PFN_encodeTiled enc = get_encode_tiled();
+  if (!enc) return false;
+  cuuint64_t d[3], strides[2];
+  cuuint32_t b[3], estr[3] = {1, 1, 1};
+  for (int i = 0; i < rank; ++i) {
+    d[i] = dims[i];
+    b[i] = box[i];
+    if (i > 0) strides[i - 1] = (i > 1 ? strides[i - 2] : 2) * dims[i - 1];
+  }
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, static_cast<cuuint32_t>(rank),
+             const_cast<void*>(ptr), d, strides, b, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 static int num_sms_current() {
   int dev = 0, n = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 0;
