@@ -46,13 +46,47 @@ __device__ __forceinline__ int block_scan(int v, int* warp_sums, int* total) {
   return v + before;
 }
 
-// One CTA.  A group has at most R / tile_rows + 1 tiles, so the counts fit an int.
+struct PlanArgs {
+  const int* off;
+  int* prefix;
+  WsHeader* hdr;
+  CUtensorMap* maps;
+  int N, R, tile_rows;
+};
+struct MapPair {
+  CUtensorMap m[2];
+};
+
+// CTA 0 counts (a group has at most R / tile_rows + 1 tiles, so the counts fit an int);
+// the others make dW's maps, a warp per group: the templates with the rows ended at
+// the group's last one.  A map's end is clipped to R whatever the offsets say.
 __global__ void __launch_bounds__(kPlanThreads)
-grouped_plan_kernel(const int* __restrict__ off, int* __restrict__ prefix, WsHeader* hdr, int N,
-                    int R, int tile_rows) {
+grouped_plan_kernel(const __grid_constant__ PlanArgs a, const __grid_constant__ MapPair templates) {
   __shared__ int warp_sums[32];
   pdl_trigger();
   pdl_wait();
+  const int* __restrict__ off = a.off;
+  int* __restrict__ prefix = a.prefix;
+  WsHeader* hdr = a.hdr;
+  const int N = a.N, R = a.R, tile_rows = a.tile_rows;
+  if (blockIdx.x > 0) {
+    const int e = (blockIdx.x - 1) * (kPlanThreads / 32) + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31;
+    if (e >= N) return;
+    const int end = min(off[e + 1], R);
+    if (end <= off[e] || end <= 0) return;       // no rows: its maps are never read
+    CUtensorMap* m = a.maps + 2 * static_cast<size_t>(e);
+    if (lane < 16)
+      reinterpret_cast<uint4*>(m)[lane] = reinterpret_cast<const uint4*>(&templates)[lane];
+    __syncwarp();
+    if (lane < 2) {
+      asm volatile("tensormap.replace.tile.global_dim.global.b1024.b32 [%0], 1, %1;" ::"l"(m + lane),
+                   "r"(end)
+                   : "memory");
+      asm volatile("fence.proxy.tensormap::generic.release.gpu;" ::: "memory");
+    }
+    return;
+  }
   int base = 0;
   bool bad = false;
   for (int e0 = 0; e0 < N; e0 += kPlanThreads) {
@@ -250,40 +284,100 @@ grouped_simt_kernel(const __grid_constant__ SimtArgs<T> p) {
 }
 
 // ---------------------------------------------------------------- bias gradient
-// One CTA per group and 32 columns: 8 interleaved runs of rows, then the runs in order.
+// A CTA sums one row tile of a group (the plan's tiles) over 32 V columns: 8
+// interleaved runs of rows (a warp each, 16-byte loads for bf16), then the runs in order.
+// A group of one tile is then done; the tiles of a larger one leave fp32 partial sums
+// that the second kernel adds in order, so a group of many rows is spread over as many
+// CTAs as it has tiles.  Bound: one read of dy.
+template <typename T>
+struct BiasVec;
+template <>
+struct BiasVec<__nv_bfloat16> {
+  static constexpr int V = 8;
+  __device__ static __forceinline__ void add(const __nv_bfloat16* p, float (&s)[V]) {
+    const uint4 q = __ldg(reinterpret_cast<const uint4*>(p));
+    const unsigned u[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      s[2 * i] += __uint_as_float(u[i] << 16);
+      s[2 * i + 1] += __uint_as_float(u[i] & 0xffff0000u);
+    }
+  }
+};
+template <>
+struct BiasVec<float> {
+  static constexpr int V = 1;       // any width, any alignment of a float
+  __device__ static __forceinline__ void add(const float* p, float (&s)[V]) { s[0] += __ldg(p); }
+};
+
 template <typename T>
 __global__ void __launch_bounds__(256)
-grouped_bias_grad_kernel(const T* __restrict__ dy, const int* __restrict__ off, T* __restrict__ db,
-                         const WsHeader* hdr, int O) {
-  __shared__ float buf[8][33];
+grouped_bias_tile_kernel(const T* __restrict__ dy, const int* __restrict__ off,
+                         const int* __restrict__ prefix, T* __restrict__ db,
+                         float* __restrict__ part, const WsHeader* hdr, int O, int N,
+                         int tile_rows) {
+  constexpr int V = BiasVec<T>::V;
+  __shared__ float buf[8][32 * V];
+  pdl_trigger();
+  pdl_wait();
+  const int q = blockIdx.x;
+  if (hdr->err || q >= prefix[N]) return;
+  const int e = find_group(prefix, N, q);
+  const int nt = q - prefix[e];
+  const int r0 = off[e] + nt * tile_rows, r1 = min(off[e + 1], r0 + tile_rows);
+  const int lane = threadIdx.x & 31, k = threadIdx.x >> 5;
+  const int c = (blockIdx.y * 32 + lane) * V;
+  float s[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) s[i] = 0.f;
+  if (c < O)
+#pragma unroll 8
+    for (int r = r0 + k; r < r1; r += 8) BiasVec<T>::add(dy + static_cast<int64_t>(r) * O + c, s);
+#pragma unroll
+  for (int i = 0; i < V; ++i) buf[k][lane + 32 * i] = s[i];
+  __syncthreads();
+  const bool one = prefix[e + 1] - prefix[e] == 1;
+  for (int x = threadIdx.x; x < 32 * V; x += 256) {
+    const int col = (blockIdx.y * 32 + (x & 31)) * V + (x >> 5);
+    if (col >= O) continue;
+    float v = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v += buf[i][x];
+    if (one) db[static_cast<int64_t>(e) * O + col] = static_cast<T>(v);
+    else part[static_cast<int64_t>(q) * O + col] = v;
+  }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(256)
+grouped_bias_sum_kernel(const int* __restrict__ prefix, T* __restrict__ db,
+                        const float* __restrict__ part, const WsHeader* hdr, int O, int N) {
   pdl_trigger();
   pdl_wait();
   if (hdr->err) return;
-  const int e = blockIdx.x, lane = threadIdx.x & 31, k = threadIdx.x >> 5;
-  const int c = blockIdx.y * 32 + lane;
-  const int r1 = off[e + 1];
+  const int c = blockIdx.y * 256 + threadIdx.x;
+  if (c >= O) return;
+  const int e = blockIdx.x, a = prefix[e], b = prefix[e + 1];
+  if (b - a == 1) return;                 // written by its tile
   float v = 0.f;
-  if (c < O)
 #pragma unroll 4
-    for (int r = off[e] + k; r < r1; r += 8) v += static_cast<float>(dy[static_cast<int64_t>(r) * O + c]);
-  buf[k][lane] = v;
-  __syncthreads();
-  if (k == 0 && c < O) {
-    v = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v += buf[i][lane];
-    db[static_cast<int64_t>(e) * O + c] = static_cast<T>(v);
-  }
+  for (int q = a; q < b; ++q) v += part[static_cast<int64_t>(q) * O + c];
+  db[static_cast<int64_t>(e) * O + c] = static_cast<T>(v);
 }
 
 }  // namespace
 
 cudaError_t launch_grouped_plan(const GroupedShape& s, const GroupedPlan& p, const int* offsets,
-                                int tile_rows, cudaStream_t stream) {
+                                int tile_rows, const CUtensorMap* maps, cudaStream_t stream) {
+  const PlanArgs a = {offsets, p.tile_prefix, p.hdr, static_cast<CUtensorMap*>(p.maps),
+                      static_cast<int>(s.N), static_cast<int>(s.R), tile_rows};
+  MapPair templates = {};
+  if (maps) templates = {{maps[0], maps[1]}};
+  constexpr int per = kPlanThreads / 32;
+  const unsigned grid = 1 + (maps ? static_cast<unsigned>((s.N + per - 1) / per) : 0);
   count_launch();
-  return launch_dependent(grouped_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, offsets,
-                          p.tile_prefix, p.hdr, static_cast<int>(s.N), static_cast<int>(s.R),
-                          tile_rows);
+  return launch_dependent(grouped_plan_kernel, dim3(grid), dim3(kPlanThreads), 0, stream, a,
+                          templates);
 }
 
 // The narrow tile when a group has at most 40 rows on average: a full tile's
@@ -320,18 +414,31 @@ cudaError_t launch_grouped_simt(const GroupedShape& s, const GroupedPlan& p, Gro
   return launch_simt<float>(s, p, which, offsets, a, b, bias, out, num_sms, stream);
 }
 
-cudaError_t launch_grouped_bias_grad(const GroupedShape& s, const GroupedPlan& p,
-                                     const int* offsets, const void* dy, void* db,
-                                     cudaStream_t stream) {
-  const dim3 grid(static_cast<unsigned>(s.N), static_cast<unsigned>((s.O + 31) / 32));
+template <typename T>
+static cudaError_t launch_bias(const GroupedShape& s, const GroupedPlan& p, const int* offsets,
+                               const void* dy, void* db, int tile_rows, cudaStream_t stream) {
+  const int O = static_cast<int>(s.O), N = static_cast<int>(s.N);
+  if (s.R > 0) {
+    const dim3 grid(static_cast<unsigned>(s.R / tile_rows + s.N),      // row tiles, at most
+                    static_cast<unsigned>((s.O + 32 * BiasVec<T>::V - 1) / (32 * BiasVec<T>::V)));
+    count_launch();
+    const cudaError_t e = launch_dependent(grouped_bias_tile_kernel<T>, grid, dim3(256), 0, stream,
+                                           static_cast<const T*>(dy), offsets, p.tile_prefix,
+                                           static_cast<T*>(db), p.bias_part, p.hdr, O, N, tile_rows);
+    if (e != cudaSuccess) return e;
+  }
   count_launch();
-  if (s.dtype == SWL_BF16)
-    return launch_dependent(grouped_bias_grad_kernel<__nv_bfloat16>, grid, dim3(256), 0, stream,
-                            static_cast<const __nv_bfloat16*>(dy), offsets,
-                            static_cast<__nv_bfloat16*>(db), p.hdr, static_cast<int>(s.O));
-  return launch_dependent(grouped_bias_grad_kernel<float>, grid, dim3(256), 0, stream,
-                          static_cast<const float*>(dy), offsets, static_cast<float*>(db), p.hdr,
-                          static_cast<int>(s.O));
+  return launch_dependent(grouped_bias_sum_kernel<T>,
+                          dim3(static_cast<unsigned>(s.N), static_cast<unsigned>((s.O + 255) / 256)),
+                          dim3(256), 0, stream, p.tile_prefix, static_cast<T*>(db), p.bias_part,
+                          p.hdr, O, N);
+}
+
+cudaError_t launch_grouped_bias_grad(const GroupedShape& s, const GroupedPlan& p,
+                                     const int* offsets, const void* dy, void* db, int tile_rows,
+                                     cudaStream_t stream) {
+  return (s.dtype == SWL_BF16 ? launch_bias<__nv_bfloat16> : launch_bias<float>)(
+      s, p, offsets, dy, db, tile_rows, stream);
 }
 
 namespace {
@@ -354,6 +461,10 @@ swl_status grouped_shape(int64_t R, int64_t K, int64_t O, int64_t N, int dtype, 
   return SWL_OK;
 }
 
+int tile_rows(const GroupedShape& s) {
+  return s.dtype == SWL_BF16 ? grouped_sm100_tile_rows(s) : grouped_simt_tile_rows(s);
+}
+
 size_t grouped_layout(const GroupedShape& s, uintptr_t base, GroupedPlan* p) {
   size_t at = 0;
   auto take = [&](size_t bytes) {
@@ -366,6 +477,8 @@ size_t grouped_layout(const GroupedShape& s, uintptr_t base, GroupedPlan* p) {
   q.tile_prefix = reinterpret_cast<int*>(take((static_cast<size_t>(s.N) + 1) * 4));
   q.maps = reinterpret_cast<void*>(
       take(s.dtype == SWL_BF16 ? static_cast<size_t>(s.N) * 2 * sizeof(CUtensorMap) : 0));
+  q.bias_part = reinterpret_cast<float*>(
+      take((static_cast<size_t>(s.R) / tile_rows(s) + s.N) * static_cast<size_t>(s.O) * 4));
   if (p) *p = q;
   return at;
 }
@@ -377,9 +490,6 @@ int grouped_sms() {
   return n;
 }
 
-int tile_rows(const GroupedShape& s) {
-  return s.dtype == SWL_BF16 ? grouped_sm100_tile_rows(s) : grouped_simt_tile_rows(s);
-}
 cudaError_t launch_product(const GroupedShape& s, const GroupedPlan& p, GroupedWhich which,
                            const int* offsets, const void* a, const void* b, const void* bias,
                            void* out, int sms, cudaStream_t stream) {
@@ -445,7 +555,7 @@ extern "C" swl_status switch_layer_grouped_matmul(int64_t R, int64_t K, int64_t 
   const int sms = grouped_sms();
   if (sms <= 0) return SWL_ERR_CUDA;
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
-  if (launch_grouped_plan(s, p, offsets, tile_rows(s), cs) != cudaSuccess)
+  if (launch_grouped_plan(s, p, offsets, tile_rows(s), nullptr, cs) != cudaSuccess)
     return SWL_ERR_CUDA;
   if (R == 0) return SWL_OK;
   if (launch_product(s, p, kGroupedFwd, offsets, x, W, bias, y, sms, cs) != cudaSuccess)
@@ -484,7 +594,10 @@ extern "C" swl_status switch_layer_grouped_matmul_backward(
   const int sms = grouped_sms();
   if (sms <= 0) return SWL_ERR_CUDA;
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
-  if (launch_grouped_plan(s, p, offsets, tile_rows(s), cs) != cudaSuccess)
+  CUtensorMap maps[2];
+  const bool map = dtype == SWL_BF16 && dW && R > 0;
+  if (map && !grouped_sm100_templates(s, dy, x, maps)) return SWL_ERR_CUDA;
+  if (launch_grouped_plan(s, p, offsets, tile_rows(s), map ? maps : nullptr, cs) != cudaSuccess)
     return SWL_ERR_CUDA;
   if (dx && R > 0 &&
       launch_product(s, p, kGroupedDx, offsets, dy, W, nullptr, dx, sms, cs) != cudaSuccess)
@@ -492,6 +605,6 @@ extern "C" swl_status switch_layer_grouped_matmul_backward(
   if (dW &&
       launch_product(s, p, kGroupedDw, offsets, dy, x, nullptr, dW, sms, cs) != cudaSuccess)
     return SWL_ERR_CUDA;
-  if (db && launch_grouped_bias_grad(s, p, offsets, dy, db, cs) != cudaSuccess) return SWL_ERR_CUDA;
+  if (db && launch_grouped_bias_grad(s, p, offsets, dy, db, tile_rows(s), cs) != cudaSuccess) return SWL_ERR_CUDA;
   return SWL_OK;
 }

@@ -19,6 +19,7 @@ struct GroupedShape {
 struct GroupedPlan {
   WsHeader* hdr;       // err, next_tile
   int* tile_prefix;    // [N + 1] row tiles of groups before e (tile_rows rows each)
+  float* bias_part;    // [row tiles, at most][O] partial bias gradients
   void* maps;          // bf16: [2 N] tensor maps, dy's and x's rows up to each group's end
 };
 
@@ -38,15 +39,17 @@ cudaError_t launch_grouped_simt(const GroupedShape& s, const GroupedPlan& p, Gro
                                 const int* offsets, const void* a, const void* b,
                                 const void* bias, void* out, int num_sms, cudaStream_t stream);
 
-// The same on the tensor cores (bf16 tensors), two launches for dW.
+// The same on the tensor cores (bf16 tensors); templates: dW's maps for the plan.
+bool grouped_sm100_templates(const GroupedShape& s, const void* dy, const void* x, CUtensorMap* out);
 int grouped_sm100_tile_rows(const GroupedShape& s);
 cudaError_t launch_grouped_sm100(const GroupedShape& s, const GroupedPlan& p, GroupedWhich which,
                                  const int* offsets, const void* a, const void* b,
                                  const void* bias, void* out, int num_sms, cudaStream_t stream);
 
-// db[e] = sum of the group's rows of dy (fp32 sums in a fixed order).
+// db[e] = sum of the group's rows of dy (fp32 sums in a fixed order); tile_rows as
+// given to the plan.
 cudaError_t launch_grouped_bias_grad(const GroupedShape& s, const GroupedPlan& p,
-                                     const int* offsets, const void* dy, void* db,
+                                     const int* offsets, const void* dy, void* db, int tile_rows,
                                      cudaStream_t stream);
 
 }  // namespace swl

@@ -8,8 +8,8 @@
 // tensor work; a single CTA's 128 x 256 tile would need 48 KB, more than the L2
 // delivers.  D lies in TMEM, lane = row of A, column = row of B:
 //   y, dx:  A = 256 features of W[e], B = the tile's token rows.  The ragged side is
-//           n, which follows the rows that are there in steps of 32 (64 for tiles of
-//           over 64 rows): a group of a few rows reads W once and multiplies little.
+//           n, which follows the rows that are there in steps of 32: a group of a few
+//           rows reads W once and multiplies little.
 //   dW:     A = 256 columns of dy, B = 256 columns of x, summed over the group's rows.
 //           The tensor maps of dy and x end at the group's last row (the plan writes a
 //           pair of maps per group): the hardware fills the rows behind it with zeros,
@@ -19,8 +19,8 @@
 // for dW).  Both come by TMA in 128-byte-swizzled boxes 64 elements wide; no operand
 // is transposed in memory.
 //
-// Roles of a CTA's 12 warps: 0 TMA producer, 1 MMA issuer (first CTA of the pair
-// only), 2 TMEM, 3 tile decoder, 4-11 epilogue (two warps per lane quarter).  Two
+// Roles of a CTA's 12 warps: 0 and 2 TMA producers of A and B, 1 MMA issuer (first CTA
+// of the pair only), 3 tile decoder, 4-11 epilogue (two warps per lane quarter).  Two
 // 256-column accumulators, so a tile's epilogue runs under the next tile's products.
 // Tiles go round the pairs in order; the row tiles of a group are consecutive.
 // Every wait is bounded: one that runs out sets the device error word and the CTA
@@ -43,7 +43,14 @@ constexpr int kMaxStages = 12;
 constexpr int kAccs = 2;
 constexpr int kTmemCols = 512;
 constexpr int kTileRing = 8;
-constexpr int kEpiBytes = kEpiWarps * 32 * 32 * 2;
+constexpr int kBand = 8;                         // row tiles of a band (2048 rows)
+constexpr int kUnit = 32;                        // rows a tile's n grows by
+// Staging of an epilogue warp: y, dx: 32 rows of 32 features; dW: 32 rows of 64 columns,
+// twice (the next rows are converted while a store reads the last ones).
+template <int W>
+constexpr int epi_bytes() {
+  return kEpiWarps * 32 * (W == kGroupedDw ? 2 * 64 : 32) * 2;
+}
 constexpr size_t kSmemLimit = 227 * 1024;
 
 struct Args {
@@ -60,9 +67,16 @@ struct Args {
   int k_blocks;    // y, dx: ceil(depth / 64)
   int m_tiles, n_tiles;   // n_tiles: dW only
   int bn;          // most rows of B per tile
-  int box;         // y, dx: rows per TMA box of B
   int stages;
   int keep_w;      // W is read by several row tiles: no evict-first
+};
+
+// The row operand of y and dx with boxes of 16, 32, .. 128 rows: a CTA's half of a
+// tile's rows comes in one copy whatever their number (four boxes of 32 rows keep the
+// copy engine too busy: 545 against 490 us for 32768 x 2048 by 8 x 5120 x 2048).
+constexpr int kBoxes = 8;
+struct RowMaps {
+  CUtensorMap box[kBoxes];
 };
 
 struct Tile {
@@ -161,8 +175,8 @@ __device__ __forceinline__ uint64_t operand_desc(uint32_t base, int k) {
 // ---------------------------------------------------------------- the kernel
 template <int W>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-grouped_sm100_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                     const __grid_constant__ Args args) {
+grouped_sm100_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ RowMaps tmB,
+                     const __grid_constant__ CUtensorMap tmOut, const __grid_constant__ Args args) {
   constexpr bool kAmn = W != kGroupedFwd, kBmn = W == kGroupedDw;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
@@ -171,8 +185,8 @@ grouped_sm100_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
   const uint32_t b_bytes = static_cast<uint32_t>(args.bn / 2) * kBK * 2;
   uint8_t* smem_a = smem;
   uint8_t* smem_b = smem_a + stages * kABytes;
-  __nv_bfloat16* epi = reinterpret_cast<__nv_bfloat16*>(smem_b + stages * b_bytes);
-  uint64_t* full = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(epi) + kEpiBytes);
+  uint8_t* epi = smem_b + stages * b_bytes;
+  uint64_t* full = reinterpret_cast<uint64_t*>(epi + epi_bytes<W>());
   uint64_t* empty = full + kMaxStages;
   uint64_t* tfull = empty + kMaxStages;
   uint64_t* tempty = tfull + kAccs;
@@ -198,14 +212,14 @@ grouped_sm100_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
     ptx::mbar_init(drain, 1);
     for (int i = 0; i < kTileRing; ++i) {
       ptx::mbar_init(&ring_full[i], 1);
-      ptx::mbar_init(&ring_empty[i], kEpiWarps + 1 + (leader ? 1 : 0));
+      ptx::mbar_init(&ring_empty[i], kEpiWarps + 2 + (leader ? 1 : 0));
     }
     *abort_flag = 0;
     ptx::fence_mbar_init();
     ptx::fence_proxy_async_smem();
     if (W != kGroupedDw) {
       ptx::prefetch_tmap(&tmA);
-      ptx::prefetch_tmap(&tmB);
+      for (int i = 0; i < kBoxes; ++i) ptx::prefetch_tmap(&tmB.box[i]);
     }
   }
   __syncthreads();
@@ -257,15 +271,24 @@ grouped_sm100_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
               else hi = mid;
             }
             const int p0 = __ldg(args.prefix + lo), nts = __ldg(args.prefix + lo + 1) - p0;
+            // bands of kBand row tiles go through all of W, row tiles fastest: the tiles
+            // running together share few rows of x and few of W
             const int local = t - p0 * args.m_tiles;
-            const int nt = local % nts;
+            const int band = local / (kBand * args.m_tiles);
+            const int r = local - band * kBand * args.m_tiles;
+            const int in_band = min(kBand, nts - band * kBand);
+            const int nt = band * kBand + r % in_band;
             ts.e = lo;
-            ts.m0 = local / nts * 256;
-            const int begin = __ldg(args.off + lo), end = __ldg(args.off + lo + 1);
-            ts.row0 = begin + nt * args.bn;
-            ts.rows = min(args.bn, end - ts.row0);
-            const int step = 2 * args.box;
-            ts.n = (ts.rows + step - 1) / step * step;
+            ts.m0 = r / in_band * 256;
+            // the group's rows in nts parts of whole units, as even as they go: no short
+            // tile that loads as much W as a full one
+            const int begin = __ldg(args.off + lo), rows = __ldg(args.off + lo + 1) - begin;
+            const int units = (rows + kUnit - 1) / kUnit;
+            const int per = units / nts, more = units - per * nts;
+            const int first = (nt * per + min(nt, more)) * kUnit;
+            ts.row0 = begin + first;
+            ts.n = (per + (nt < more ? 1 : 0)) * kUnit;
+            ts.rows = min(ts.n, rows - first);
             ts.kb = args.k_blocks;
           }
         }
@@ -275,14 +298,18 @@ grouped_sm100_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
       }
     }
     __syncwarp();
-  } else if (warp == 0) {
-    // ------------------------------------------------------------ producer
+  } else if (warp == 0 || warp == 2) {
+    // ------------------------------------------------------------ producers
+    // Warp 0 loads A (and, in the first CTA, announces the stage's bytes), warp 2
+    // loads B: one thread for both is not fast enough for full tiles.
     if (lane == 0) {
-      const uint64_t keep = ptx::l2_policy_evict_last();
+      const bool is_a = warp == 0;
       const uint64_t norm = l2_policy_normal();
-      const uint64_t pol_a = W == kGroupedDw || args.keep_w ? norm : ptx::l2_policy_evict_first();
-      const uint64_t pol_b = W == kGroupedDw ? norm : keep;
-      int stage = 0;
+      const uint64_t pol = W == kGroupedDw || (is_a && args.keep_w)
+                               ? norm
+                               : is_a ? ptx::l2_policy_evict_first() : ptx::l2_policy_evict_last();
+      const uint32_t bar0 = leader_addr(&full[0]);
+      int stage = 0, last_e = -1;
       uint32_t ph = 0;
       bool ok = true;
       for (int i = 0; ok; ++i) {
@@ -295,17 +322,17 @@ grouped_sm100_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
         const Tile ts = ring[slot];
         ptx::mbar_arrive(&ring_empty[slot]);
         if (ts.t < 0) break;
-        const CUtensorMap* mapA = &tmA;
-        const CUtensorMap* mapB = &tmB;
+        const CUtensorMap* map = &tmA;
         if constexpr (W == kGroupedDw) {
-          mapA = args.maps + 2 * ts.e;
-          mapB = mapA + 1;
-          // the maps were written by another kernel's ordinary stores
-          asm volatile("fence.proxy.tensormap::generic.acquire.gpu [%0], 128;" ::"l"(mapA) : "memory");
-          asm volatile("fence.proxy.tensormap::generic.acquire.gpu [%0], 128;" ::"l"(mapB) : "memory");
+          // written by another kernel's ordinary stores
+          map = args.maps + 2 * ts.e + (is_a ? 0 : 1);
+          if (ts.e != last_e)
+            asm volatile("fence.proxy.tensormap::generic.acquire.gpu [%0], 128;" ::"l"(map) : "memory");
+          last_e = ts.e;
         }
         const int half = ts.n >> 1;              // this CTA's rows of B
         const int m0 = ts.m0 + static_cast<int>(rank) * 128;
+        const int b0 = (W == kGroupedDw ? ts.n0 : ts.row0) + static_cast<int>(rank) * half;
         const uint32_t bytes = 2 * (kABytes + static_cast<uint32_t>(half) * kBK * 2);
         for (int kb = 0; kb < ts.kb; ++kb) {
           if (!ptx::mbar_wait(&empty[stage], ph ^ 1u, abort_flag, args.wait_ns)) {
@@ -313,27 +340,27 @@ grouped_sm100_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
             ok = false;
             break;
           }
-          if (leader) ptx::mbar_arrive_expect_tx(&full[stage], bytes);
-          const uint32_t bar = leader_addr(&full[stage]);
-          uint8_t* a = smem_a + stage * kABytes;
-          uint8_t* b = smem_b + stage * b_bytes;
-          if constexpr (W == kGroupedFwd) {
-            pair_load_3d(a, mapA, bar, kb * kBK, m0, ts.e, pol_a);
-          } else if constexpr (W == kGroupedDx) {
-            pair_load_3d(a, mapA, bar, m0, kb * kBK, ts.e, pol_a);
-            pair_load_3d(a + 8192, mapA, bar, m0 + 64, kb * kBK, ts.e, pol_a);
+          const uint32_t bar = bar0 + stage * 8;
+          if (is_a) {
+            if (leader) ptx::mbar_arrive_expect_tx(&full[stage], bytes);
+            uint8_t* a = smem_a + stage * kABytes;
+            if constexpr (W == kGroupedFwd) {
+              pair_load_3d(a, map, bar, kb * kBK, m0, ts.e, pol);
+            } else if constexpr (W == kGroupedDx) {
+              pair_load_3d(a, map, bar, m0, kb * kBK, ts.e, pol);
+              pair_load_3d(a + 8192, map, bar, m0 + 64, kb * kBK, ts.e, pol);
+            } else {
+              pair_load_2d(a, map, bar, m0, ts.row0 + kb * kBK, pol);
+              pair_load_2d(a + 8192, map, bar, m0 + 64, ts.row0 + kb * kBK, pol);
+            }
           } else {
-            pair_load_2d(a, mapA, bar, m0, ts.row0 + kb * kBK, pol_a);
-            pair_load_2d(a + 8192, mapA, bar, m0 + 64, ts.row0 + kb * kBK, pol_a);
-          }
-          if constexpr (W == kGroupedDw) {
-            const int n0 = ts.n0 + static_cast<int>(rank) * half;
-            for (int j = 0; j < half; j += 64)
-              pair_load_2d(b + j * 128, mapB, bar, n0 + j, ts.row0 + kb * kBK, pol_b);
-          } else {
-            const int r0 = ts.row0 + static_cast<int>(rank) * half;
-            for (int j = 0; j < half; j += args.box)
-              pair_load_2d(b + j * 128, mapB, bar, kb * kBK, r0 + j, pol_b);
+            uint8_t* b = smem_b + stage * b_bytes;
+            if constexpr (W == kGroupedDw) {
+              for (int j = 0; j < half; j += 64)
+                pair_load_2d(b + j * 128, map, bar, b0 + j, ts.row0 + kb * kBK, pol);
+            } else {
+              pair_load_2d(b, &tmB.box[half / 16 - 1], bar, kb * kBK, b0, pol);
+            }
           }
           if (++stage == stages) {
             stage = 0;
@@ -409,10 +436,12 @@ grouped_sm100_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
   } else if (warp >= 4) {
     // ------------------------------------------------------------ epilogue
     const int q = warp & 3, side = (warp - 4) >> 2;
-    __nv_bfloat16* st = epi + (warp - 4) * 32 * 32;      // [32 rows][32 features]
+    uint8_t* const stage_out = epi + (warp - 4) * (epi_bytes<W>() / kEpiWarps);
+    __nv_bfloat16* const st = reinterpret_cast<__nv_bfloat16*>(stage_out);
     const uint32_t tempty0 = leader_addr(&tempty[0]), tempty1 = leader_addr(&tempty[1]);
     int acc = 0;
     uint32_t aph = 0;
+    bool flip = false;
     for (int i = 0;; ++i) {
       const int slot = i % kTileRing;
       if (!__all_sync(0xffffffffu, ptx::mbar_wait(&ring_full[slot], (i / kTileRing) & 1, abort_flag,
@@ -436,31 +465,54 @@ grouped_sm100_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
         }
         ptx::tc_fence_after();
       }
-      const int width = W == kGroupedDw ? min(ts.n, args.cols - ts.n0) : ts.rows;
-      for (int c0 = side * 32; c0 < width; c0 += 64) {
-        uint32_t r[32];
-        if (ts.kb > 0) {
+      if constexpr (W == kGroupedDw) {
+        // 64 columns at a time: a lane converts its row, the rows go out by a TMA store
+        // from 128-byte-swizzled staging (whole 128-byte lines; rows and columns past the
+        // end of the group's matrix are not written)
+        const int width = min(ts.n, args.cols - ts.n0);
+        for (int c0 = side * 64; c0 < width; c0 += 128) {
+          uint32_t r[2][32];
+          if (ts.kb > 0) {
+            ptx::tmem_ld_32x32b_x32(t0 + static_cast<uint32_t>(c0), r[0]);
+            ptx::tmem_ld_32x32b_x32(t0 + static_cast<uint32_t>(c0 + 32), r[1]);
+            ptx::tmem_ld_wait();
+          } else {
+#pragma unroll
+            for (int j = 0; j < 64; ++j) r[j >> 5][j & 31] = 0u;
+          }
+          // this half of the staging is free once the store before the last has read it
+          uint8_t* const half_out = stage_out + (flip ? 4096 : 0);
+          flip = !flip;
+          if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+          __syncwarp();
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            __nv_bfloat162 v[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int c = j * 8 + 2 * k;
+              v[k] = __floats2bfloat162_rn(__uint_as_float(r[c >> 5][c & 31]),
+                                           __uint_as_float(r[(c + 1) >> 5][(c + 1) & 31]));
+            }
+            *reinterpret_cast<uint4*>(half_out + lane * 128 + ((j ^ (lane & 7)) << 4)) =
+                *reinterpret_cast<const uint4*>(v);
+          }
+          ptx::fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            if (f0 < args.m) asm volatile(
+                "cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                    reinterpret_cast<uint64_t>(&tmOut)),
+                "r"(ptx::smem_u32(half_out)), "r"(ts.n0 + c0), "r"(f0), "r"(ts.e)
+                : "memory");
+            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+          }
+        }
+      } else {
+        for (int c0 = side * 32; c0 < ts.rows; c0 += 64) {
+          uint32_t r[32];
           ptx::tmem_ld_32x32b_x32(t0 + static_cast<uint32_t>(c0), r);
           ptx::tmem_ld_wait();
-        } else {
-#pragma unroll
-          for (int j = 0; j < 32; ++j) r[j] = 0u;
-        }
-        if constexpr (W == kGroupedDw) {
-          // a lane's 32 columns are consecutive in memory
-          if (f < args.m) {
-            __nv_bfloat16* o = args.out + (static_cast<size_t>(ts.e) * args.m + f) * args.cols + ts.n0 + c0;
-#pragma unroll
-            for (int j = 0; j < 32; j += 8) {
-              if (c0 + j >= width) break;       // cols % 8 == 0
-              __nv_bfloat162 v[4];
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                v[k] = __floats2bfloat162_rn(__uint_as_float(r[j + 2 * k]), __uint_as_float(r[j + 2 * k + 1]));
-              *reinterpret_cast<uint4*>(o + j) = *reinterpret_cast<const uint4*>(v);
-            }
-          }
-        } else {
 #pragma unroll
           for (int j = 0; j < 32; j += 2) {     // two rows per conversion
             const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(r[j]) + bias,
@@ -492,6 +544,7 @@ grouped_sm100_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
         aph ^= 1u;
       }
     }
+    if (W == kGroupedDw && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   }
   __syncwarp();
   ptx::tc_fence_before();
@@ -502,43 +555,25 @@ grouped_sm100_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
   }
 }
 
-// ---------------------------------------------------------------- dW's maps
-// One warp per group: the two template maps with the rows ended at offsets[e + 1].
-__global__ void __launch_bounds__(256)
-grouped_maps_kernel(const __grid_constant__ CUtensorMap dy, const __grid_constant__ CUtensorMap x,
-                    CUtensorMap* __restrict__ maps, const int* __restrict__ off,
-                    const WsHeader* hdr, int N) {
-  pdl_trigger();
-  pdl_wait();
-  const int e = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  if (e >= N || hdr->err) return;
-  const int end = off[e + 1];
-  if (end <= off[e]) return;             // no rows: its maps are never read
-  CUtensorMap* m = maps + 2 * e;
-  if (lane < 16)
-    reinterpret_cast<uint4*>(m)[lane] =
-        reinterpret_cast<const uint4*>(lane < 8 ? &dy : &x)[lane & 7];
-  __syncwarp();
-  if (lane < 2) {
-    asm volatile("tensormap.replace.tile.global_dim.global.b1024.b32 [%0], 1, %1;" ::"l"(m + lane),
-                 "r"(end)
-                 : "memory");
-    asm volatile("fence.proxy.tensormap::generic.release.gpu;" ::: "memory");
-  }
-}
-
 }  // namespace
 
+bool grouped_sm100_templates(const GroupedShape& s, const void* dy, const void* x, CUtensorMap* out) {
+  const uint64_t dd[2] = {static_cast<uint64_t>(s.O), static_cast<uint64_t>(s.R)};
+  const uint64_t dx[2] = {static_cast<uint64_t>(s.K), static_cast<uint64_t>(s.R)};
+  const uint32_t box[2] = {64, 64};
+  return encode_tmap_bf16(&out[0], dy, 2, dd, box) && encode_tmap_bf16(&out[1], x, 2, dx, box);
+}
+
 // Rows of B per tile, at most: 256 once the groups have 48 rows on average (one pass
-// over W for most), fewer for few rows (more stages fit, and n follows the rows in
-// steps of 32 instead of 64).
+// over W for most), 64 for fewer rows (more stages of W fit).
 int grouped_sm100_tile_rows(const GroupedShape& s) { return s.R >= 48 * s.N ? 256 : 64; }
 
 cudaError_t launch_grouped_sm100(const GroupedShape& s, const GroupedPlan& p, GroupedWhich which,
                                  const int* offsets, const void* a, const void* b,
                                  const void* bias, void* out, int num_sms, cudaStream_t stream) {
   const uint64_t K = s.K, O = s.O, N = s.N, R = s.R;
-  CUtensorMap mapA, mapB;
+  CUtensorMap mapA = {}, mapOut = {};
+  RowMaps rows = {};
   Args g = {};
   g.off = offsets;
   g.prefix = p.tile_prefix;
@@ -550,37 +585,25 @@ cudaError_t launch_grouped_sm100(const GroupedShape& s, const GroupedPlan& p, Gr
   g.N = static_cast<int>(N);
   int64_t tiles;      // at most
   if (which == kGroupedDw) {
-    const uint64_t da[2] = {O, R}, db[2] = {K, R};
-    const uint32_t box[2] = {64, 64};
-    // rows 0 (an empty batch): every group is empty, the maps are not made
-    if (R > 0) {
-      if (!encode_tmap_bf16(&mapA, a, 2, da, box) || !encode_tmap_bf16(&mapB, b, 2, db, box))
-        return cudaErrorInvalidValue;
-      count_launch();
-      const cudaError_t e =
-          launch_dependent(grouped_maps_kernel, dim3(static_cast<unsigned>((N + 7) / 8)), dim3(256),
-                           0, stream, mapA, mapB, static_cast<CUtensorMap*>(p.maps), offsets,
-                           p.hdr, g.N);
-      if (e != cudaSuccess) return e;
-    } else {
-      mapA = mapB = CUtensorMap{};
-    }
+    const uint64_t dout[3] = {K, O, N};
+    const uint32_t bout[3] = {64, 32, 1};
+    if (!encode_tmap_bf16(&mapOut, out, 3, dout, bout)) return cudaErrorInvalidValue;
     g.m = static_cast<int>(O);
     g.cols = static_cast<int>(K);
     g.n_tiles = static_cast<int>((K + 255) / 256);
     g.bn = K <= 128 ? 128 : 256;
-    g.box = 64;
     g.m_tiles = (g.m + 255) / 256;
     tiles = static_cast<int64_t>(N) * g.m_tiles * g.n_tiles;
   } else {
     const uint64_t dw[3] = {K, O, N}, dr[2] = {which == kGroupedFwd ? K : O, R};
     const uint32_t bw[3] = {64, which == kGroupedFwd ? 128u : 64u, 1};
     g.bn = grouped_sm100_tile_rows(s);
-    g.box = g.bn > 64 ? 32 : 16;
-    const uint32_t br[2] = {64, static_cast<uint32_t>(g.box)};
     // a is the row operand (x, dy), b is W
-    if (!encode_tmap_bf16(&mapA, b, 3, dw, bw) || !encode_tmap_bf16(&mapB, a, 2, dr, br))
-      return cudaErrorInvalidValue;
+    if (!encode_tmap_bf16(&mapA, b, 3, dw, bw)) return cudaErrorInvalidValue;
+    for (int i = 0; i < kBoxes; ++i) {
+      const uint32_t br[2] = {64, 16u * (i + 1)};
+      if (!encode_tmap_bf16(&rows.box[i], a, 2, dr, br)) return cudaErrorInvalidValue;
+    }
     g.m = static_cast<int>(which == kGroupedFwd ? O : K);
     g.k_blocks = static_cast<int>((dr[0] + kBK - 1) / kBK);
     g.m_tiles = (g.m + 255) / 256;
@@ -588,7 +611,7 @@ cudaError_t launch_grouped_sm100(const GroupedShape& s, const GroupedPlan& p, Gr
     tiles = (s.R / g.bn + s.N) * g.m_tiles;
   }
   const size_t stage = kABytes + static_cast<size_t>(g.bn / 2) * kBK * 2;
-  const size_t fixed = 1024 + kEpiBytes + (2 * kMaxStages + 2 * kAccs + 1 + 2 * kTileRing) * 8 +
+  const size_t fixed = 1024 + (which == kGroupedDw ? epi_bytes<kGroupedDw>() : epi_bytes<kGroupedFwd>()) + (2 * kMaxStages + 2 * kAccs + 1 + 2 * kTileRing) * 8 +
                        kTileRing * sizeof(Tile) + 64;
   int stages = static_cast<int>((kSmemLimit - fixed) / stage);
   g.stages = stages < kMaxStages ? stages : kMaxStages;
@@ -602,7 +625,7 @@ cudaError_t launch_grouped_sm100(const GroupedShape& s, const GroupedPlan& p, Gr
   const int64_t pairs = num_sms / 2;
   count_launch();
   return launch_dependent(kernel, dim3(static_cast<unsigned>(2 * (tiles < pairs ? tiles : pairs))),
-                          dim3(kThreads), smem, stream, mapA, mapB, g);
+                          dim3(kThreads), smem, stream, mapA, rows, mapOut, g);
 }
 
 }  // namespace swl
