@@ -248,7 +248,7 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
 
 def _stream_handle(stream) -> int:
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
@@ -821,10 +821,13 @@ def _at(t: Optional[torch.Tensor], name: str, dtype, shape, dev) -> Optional[int
     return t.data_ptr()
 
 
+_HERE_ALREADY = contextlib.nullcontext()
+
+
 def _on(dev: torch.device):
     """A context in which ``dev`` is the current device (the library launches there)."""
-    if dev.index is None or dev.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
+    if dev.index is None or dev.index == torch._C._cuda_getDevice():
+        return _HERE_ALREADY
     return torch.cuda.device(dev)
 
 
@@ -832,7 +835,7 @@ def _allocating_on(stream, dev: torch.device):
     """A context in which torch allocates for ``stream`` (None: the current one), so that
     memory freed after the call is not handed out before the stream is done with it."""
     if stream is None:
-        return contextlib.nullcontext()
+        return _HERE_ALREADY
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(int(stream), device=dev)
     return torch.cuda.stream(stream)

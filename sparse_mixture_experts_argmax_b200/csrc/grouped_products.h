@@ -46,6 +46,13 @@ cudaError_t launch_grouped_sm100(const GroupedShape& s, const GroupedPlan& p, Gr
                                  const int* offsets, const void* a, const void* b,
                                  const void* bias, void* out, int num_sms, cudaStream_t stream);
 
+// The forward product for at most kFewRows rows, without a plan: checks the offsets
+// and writes the device status itself.
+constexpr int kFewRows = 16;
+cudaError_t launch_grouped_few(const GroupedShape& s, const GroupedPlan& p, const int* offsets,
+                               const void* x, const void* W, const void* bias, void* y,
+                               cudaStream_t stream);
+
 // db[e] = sum of the group's rows of dy (fp32 sums in a fixed order); tile_rows as
 // given to the plan.
 cudaError_t launch_grouped_bias_grad(const GroupedShape& s, const GroupedPlan& p,
