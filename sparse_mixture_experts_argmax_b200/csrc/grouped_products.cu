@@ -1,5 +1,5 @@
-// Products grouped by expert over ragged row ranges: the plan kernel, the
-// products on the CUDA cores, the bias gradient and the C entry points.
+// Products grouped by expert over ragged row ranges: the plan kernel, the bias
+// gradient and the C entry points.
 //
 // Group e owns the rows offsets[e] <= r < offsets[e + 1] of x [R, K], y [R, O]:
 //   y[r]  = W[e] x[r] + b[e]                  W [N, O, K], b [N, O]
@@ -123,166 +123,6 @@ __device__ __forceinline__ int find_group(const int* __restrict__ P, int N, int 
   return lo;
 }
 
-// ---------------------------------------------------------------- CUDA-core products
-// C[m, n] = sum_k A(m, k) B(n, k): a CTA of 16 x 16 threads computes a TM x 128
-// tile, TM / 16 x 8 values per thread, in steps of 16 along k.  The operands of a
-// step go through shared memory (k-major, two buffers); the next step's are read
-// into registers under the arithmetic.  Bound: fp32 FMA issue for full tiles
-// (TM = 128: 64 FMAs per four 16-byte shared loads); W's bytes for groups of a few
-// rows, for which the narrow tile (TM = 32) wastes fewer FMAs on missing rows.
-constexpr int kTN = 128, kTK = 16;
-constexpr int kSimtThreads = 256;
-
-template <typename T>
-struct SimtArgs {
-  const T* a;
-  const T* b;
-  const T* bias;
-  T* out;
-  const int* off;
-  const int* prefix;
-  const WsHeader* hdr;
-  int K, O, N;
-};
-
-template <typename T, int W, int TM>
-__global__ void __launch_bounds__(kSimtThreads, TM == 128 ? 2 : 3)
-grouped_simt_kernel(const __grid_constant__ SimtArgs<T> p) {
-  // k-contiguous operands: A for y and dx, B for y; else the tile's index is
-  constexpr bool kAk = W != kGroupedDw, kBk = W == kGroupedFwd;
-  constexpr int RM = TM / 16;
-  __shared__ __align__(16) float sA[2][kTK][TM + 4], sB[2][kTK][kTN + 4];
-  pdl_trigger();
-  pdl_wait();
-  const int tid = threadIdx.x;
-  const int tx = tid & 15, ty = tid >> 4;
-  const int n_cols = W == kGroupedFwd ? p.O : p.K;          // columns of the output
-  const int n_tiles = (n_cols + kTN - 1) / kTN;
-  const int m_tiles_w = (p.O + TM - 1) / TM;                // row tiles of dW[e]
-  const int total = W == kGroupedDw ? (p.hdr->err ? 0 : p.N * m_tiles_w * n_tiles)
-                                    : p.prefix[p.N] * n_tiles;
-  for (int t = blockIdx.x; t < total; t += gridDim.x) {
-    int e, m0, n0, m_end, row0 = 0, kn;
-    if constexpr (W == kGroupedDw) {
-      e = t / (m_tiles_w * n_tiles);
-      const int r = t - e * m_tiles_w * n_tiles;
-      m0 = r / n_tiles * TM;
-      n0 = (r % n_tiles) * kTN;
-      m_end = p.O;
-      row0 = p.off[e];
-      kn = p.off[e + 1] - row0;
-    } else {
-      // within a group: row tiles fastest, so the CTAs running together share W
-      const int q = t / n_tiles;
-      e = find_group(p.prefix, p.N, q);
-      const int p0 = p.prefix[e], nts = p.prefix[e + 1] - p0;
-      const int local = t - p0 * n_tiles;
-      n0 = local / nts * kTN;
-      m0 = (local % nts) * TM;
-      row0 = p.off[e];
-      m_end = p.off[e + 1] - row0;
-      kn = W == kGroupedFwd ? p.K : p.O;
-    }
-    const T* A;
-    const T* B;
-    int64_t lda, ldb;
-    if constexpr (W == kGroupedFwd) {
-      A = p.a + static_cast<int64_t>(row0) * p.K, lda = p.K;
-      B = p.b + static_cast<int64_t>(e) * p.O * p.K, ldb = p.K;
-    } else if constexpr (W == kGroupedDx) {
-      A = p.a + static_cast<int64_t>(row0) * p.O, lda = p.O;
-      B = p.b + static_cast<int64_t>(e) * p.O * p.K, ldb = p.K;
-    } else {
-      A = p.a + static_cast<int64_t>(row0) * p.O, lda = p.O;
-      B = p.b + static_cast<int64_t>(row0) * p.K, ldb = p.K;
-    }
-    // A value (index i of the tile dimension, k) per load; consecutive threads take
-    // consecutive addresses
-    constexpr int LA = TM * kTK / kSimtThreads, LB = kTN * kTK / kSimtThreads;
-    float ra[LA], rb[LB];
-    auto load = [&](int k0) {
-#pragma unroll
-      for (int j = 0; j < LA; ++j) {
-        const int x = tid + j * kSimtThreads;
-        const int i = kAk ? x / kTK : x % TM, k = kAk ? x % kTK : x / TM;
-        ra[j] = (m0 + i < m_end && k0 + k < kn)
-                    ? static_cast<float>(kAk ? A[(m0 + i) * lda + k0 + k] : A[(k0 + k) * lda + m0 + i])
-                    : 0.f;
-      }
-#pragma unroll
-      for (int j = 0; j < LB; ++j) {
-        const int x = tid + j * kSimtThreads;
-        const int i = kBk ? x / kTK : x % kTN, k = kBk ? x % kTK : x / kTN;
-        rb[j] = (n0 + i < n_cols && k0 + k < kn)
-                    ? static_cast<float>(kBk ? B[(n0 + i) * ldb + k0 + k] : B[(k0 + k) * ldb + n0 + i])
-                    : 0.f;
-      }
-    };
-    auto store = [&](int s) {
-#pragma unroll
-      for (int j = 0; j < LA; ++j) {
-        const int x = tid + j * kSimtThreads;
-        sA[s][kAk ? x % kTK : x / TM][kAk ? x / kTK : x % TM] = ra[j];
-      }
-#pragma unroll
-      for (int j = 0; j < LB; ++j) {
-        const int x = tid + j * kSimtThreads;
-        sB[s][kBk ? x % kTK : x / kTN][kBk ? x / kTK : x % kTN] = rb[j];
-      }
-    };
-    float c[RM][8];
-#pragma unroll
-    for (int i = 0; i < RM; ++i)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) c[i][j] = 0.f;
-    if (kn > 0) {
-      load(0);
-      store(0);
-    }
-    __syncthreads();
-    int s = 0;
-    for (int k0 = 0; k0 < kn; k0 += kTK) {
-      const bool more = k0 + kTK < kn;
-      if (more) load(k0 + kTK);
-#pragma unroll
-      for (int k = 0; k < kTK; ++k) {
-        float a[RM], b[8];
-        // columns 4 tx and 64 + 4 tx on: a quarter-warp reads consecutive 16-byte words
-        *reinterpret_cast<float4*>(b) = *reinterpret_cast<const float4*>(&sB[s][k][tx * 4]);
-        *reinterpret_cast<float4*>(b + 4) = *reinterpret_cast<const float4*>(&sB[s][k][64 + tx * 4]);
-        if constexpr (RM == 8) {
-          *reinterpret_cast<float4*>(a) = *reinterpret_cast<const float4*>(&sA[s][k][ty * 8]);
-          *reinterpret_cast<float4*>(a + 4) = *reinterpret_cast<const float4*>(&sA[s][k][ty * 8 + 4]);
-        } else {
-          *reinterpret_cast<float2*>(a) = *reinterpret_cast<const float2*>(&sA[s][k][ty * 2]);
-        }
-#pragma unroll
-        for (int i = 0; i < RM; ++i)
-#pragma unroll
-          for (int j = 0; j < 8; ++j) c[i][j] = fmaf(a[i], b[j], c[i][j]);
-      }
-      if (more) store(s ^ 1);
-      __syncthreads();
-      s ^= 1;
-    }
-#pragma unroll
-    for (int i = 0; i < RM; ++i) {
-      const int m = m0 + ty * RM + i;
-      if (m >= m_end) continue;
-      T* o = W == kGroupedDw ? p.out + (static_cast<int64_t>(e) * p.O + m) * p.K
-                                 : p.out + (static_cast<int64_t>(row0) + m) * n_cols;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int n = n0 + (j < 4 ? tx * 4 + j : 64 + tx * 4 + j - 4);
-        if (n >= n_cols) continue;
-        float v = c[i][j];
-        if (W == kGroupedFwd && p.bias) v += static_cast<float>(p.bias[static_cast<int64_t>(e) * p.O + n]);
-        o[n] = static_cast<T>(v);
-      }
-    }
-  }
-}
-
 // ---------------------------------------------------------------- bias gradient
 // A CTA sums one row tile of a group (the plan's tiles) over 32 V columns: 8
 // interleaved runs of rows (a warp each, 16-byte loads for bf16), then the runs in order.
@@ -380,40 +220,6 @@ cudaError_t launch_grouped_plan(const GroupedShape& s, const GroupedPlan& p, con
                           templates);
 }
 
-// The narrow tile when a group has at most 40 rows on average: a full tile's
-// missing rows then cost more than the narrow tile's smaller reuse.
-int grouped_simt_tile_rows(const GroupedShape& s) { return s.R > 40 * s.N ? 128 : 32; }
-
-template <typename T>
-static cudaError_t launch_simt(const GroupedShape& s, const GroupedPlan& p, GroupedWhich which,
-                               const int* offsets, const void* a, const void* b, const void* bias,
-                               void* out, int num_sms, cudaStream_t stream) {
-  const SimtArgs<T> args = {static_cast<const T*>(a), static_cast<const T*>(b),
-                            static_cast<const T*>(bias), static_cast<T*>(out), offsets,
-                            p.tile_prefix, p.hdr, static_cast<int>(s.K), static_cast<int>(s.O),
-                            static_cast<int>(s.N)};
-  const int tm = which == kGroupedDw ? 128 : grouped_simt_tile_rows(s);
-  const int64_t cols = which == kGroupedFwd ? s.O : s.K;
-  const int64_t col_tiles = (cols + kTN - 1) / kTN;
-  const int64_t tiles = which == kGroupedDw ? s.N * ((s.O + 127) / 128) * col_tiles
-                                            : (s.R / tm + s.N) * col_tiles;   // at most
-  const int64_t most = static_cast<int64_t>(num_sms) * (tm == 128 ? 2 : 3);
-  const dim3 grid(static_cast<unsigned>(tiles < most ? tiles : most));
-  auto* kernel = which == kGroupedDw   ? grouped_simt_kernel<T, kGroupedDw, 128>
-                 : which == kGroupedDx ? (tm == 128 ? grouped_simt_kernel<T, kGroupedDx, 128>
-                                                    : grouped_simt_kernel<T, kGroupedDx, 32>)
-                                       : (tm == 128 ? grouped_simt_kernel<T, kGroupedFwd, 128>
-                                                    : grouped_simt_kernel<T, kGroupedFwd, 32>);
-  count_launch();
-  return launch_dependent(kernel, grid, dim3(kSimtThreads), 0, stream, args);
-}
-
-cudaError_t launch_grouped_simt(const GroupedShape& s, const GroupedPlan& p, GroupedWhich which,
-                                const int* offsets, const void* a, const void* b,
-                                const void* bias, void* out, int num_sms, cudaStream_t stream) {
-  return launch_simt<float>(s, p, which, offsets, a, b, bias, out, num_sms, stream);
-}
-
 template <typename T>
 static cudaError_t launch_bias(const GroupedShape& s, const GroupedPlan& p, const int* offsets,
                                const void* dy, void* db, int tile_rows, cudaStream_t stream) {
@@ -462,7 +268,7 @@ swl_status grouped_shape(int64_t R, int64_t K, int64_t O, int64_t N, int dtype, 
 }
 
 int tile_rows(const GroupedShape& s) {
-  return s.dtype == SWL_BF16 ? grouped_sm100_tile_rows(s) : grouped_simt_tile_rows(s);
+  return s.dtype == SWL_BF16 ? grouped_sm100_tile_rows(s) : grouped_f32_tile_rows();
 }
 
 size_t grouped_layout(const GroupedShape& s, uintptr_t base, GroupedPlan* p) {
@@ -493,7 +299,7 @@ int grouped_sms() {
 cudaError_t launch_product(const GroupedShape& s, const GroupedPlan& p, GroupedWhich which,
                            const int* offsets, const void* a, const void* b, const void* bias,
                            void* out, int sms, cudaStream_t stream) {
-  return (s.dtype == SWL_BF16 ? launch_grouped_sm100 : launch_grouped_simt)(
+  return (s.dtype == SWL_BF16 ? launch_grouped_sm100 : launch_grouped_f32)(
       s, p, which, offsets, a, b, bias, out, sms, stream);
 }
 

@@ -31,15 +31,15 @@ enum GroupedWhich : int { kGroupedFwd = 0, kGroupedDx = 1, kGroupedDw = 2 };
 cudaError_t launch_grouped_plan(const GroupedShape& s, const GroupedPlan& p, const int* offsets,
                                 int tile_rows, cudaStream_t stream);
 
-// Products on the CUDA cores in fp32.  which: y = x W^T + b
-// (kGroupedFwd: a = x, b = W, bias), dx = dy W (kGroupedDx: a = dy, b = W) or
-// dW = dy^T x (kGroupedDw: a = dy, b = x; every group written, empty ones zero).
-int grouped_simt_tile_rows(const GroupedShape& s);
-cudaError_t launch_grouped_simt(const GroupedShape& s, const GroupedPlan& p, GroupedWhich which,
-                                const int* offsets, const void* a, const void* b,
-                                const void* bias, void* out, int num_sms, cudaStream_t stream);
+// The products of fp32 tensors.  which: y = x W^T + b (kGroupedFwd: a = x, b = W,
+// bias), dx = dy W (kGroupedDx: a = dy, b = W) or dW = dy^T x (kGroupedDw: a = dy, b = x;
+// every group written, empty ones zero).
+int grouped_f32_tile_rows();
+cudaError_t launch_grouped_f32(const GroupedShape& s, const GroupedPlan& p, GroupedWhich which,
+                               const int* offsets, const void* a, const void* b, const void* bias,
+                               void* out, int num_sms, cudaStream_t stream);
 
-// The same on the tensor cores (bf16 tensors); templates: dW's maps for the plan.
+// The same of bf16 tensors; templates: dW's maps for the plan.
 bool grouped_sm100_templates(const GroupedShape& s, const void* dy, const void* x, CUtensorMap* out);
 int grouped_sm100_tile_rows(const GroupedShape& s);
 cudaError_t launch_grouped_sm100(const GroupedShape& s, const GroupedPlan& p, GroupedWhich which,

@@ -1,0 +1,471 @@
+// Products grouped by expert on the tensor cores for fp32 tensors: y = x W^T + b,
+// dx = dy W and dW = dy^T x over ragged row ranges.
+//
+// An fp32 number is the sum of three bf16 numbers exactly: x rounded to 8 significant
+// bits, the rest rounded to 8, and the rest of that, which fits 8 (x = hi + mid + lo;
+// |mid| <= 2^-8 |x|, |lo| <= 2^-16 |x|; the pieces of a number that is not finite are the
+// number and zeros).  A product is then six bf16 products, each exact in fp32,
+//   lo hi' + hi lo' + mid mid' + mid hi' + hi mid' + hi hi',
+// the three left out being at most 2^-23 of it together.  Six tensor-core products cost
+// 0.1 of one fp32 FMA per term at these units' rates (1.64 PFLOP/s against 75 TFLOP/s).
+//
+// The tensor cores cut their running sums instead of rounding them, so a long sum
+// would drift by half a unit per step.  Sums in TMEM therefore run over 64 terms only,
+// the small products first (their sum is 2^-7 of the whole, so cutting it costs
+// nothing); the epilogue warps add the partial sums up in registers, rounded.
+//
+// A pair of CTAs (cta_group::2) computes D[256, n], n <= 128; lane = row of A:
+//   y, dx:  A = 256 features of W[e], B = the tile's token rows (n follows them)
+//   dW:     A = 256 columns of x, B = 128 columns of dy, summed over the group's rows
+// so that the 32 lanes of a store are consecutive in memory and no staging is needed.
+// Bound: the converting warps read fp32 operands from memory (any alignment, any width;
+// columns and rows past the end become zeros), split them and store three
+// 128-byte-swizzled tiles each, 24 instructions per 4 elements; at n = 128 the six
+// products of a 64-deep step take 1536 cycles and its 12288 elements about 900 issue
+// cycles, for fewer rows the loads bound it.
+//
+// Roles of a CTA's 20 warps: 0 MMA issuer (first CTA only), 1 TMEM, 2 tile decoder,
+// 4-11 sums and stores (two warps per lane quarter), 12-19 converters.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "grouped_sm100.cuh"
+
+namespace swl {
+namespace {
+
+constexpr int kSumWarps = 8, kConvWarps = 8;
+constexpr int kThreads = 128 + 32 * (kSumWarps + kConvWarps);
+constexpr int kBN = 128;                               // most rows of B per tile
+constexpr uint32_t kAPlane = 128 * kBK * 2;            // a CTA's half of A, one piece
+constexpr uint32_t kBPlane = kBN / 2 * kBK * 2;
+constexpr uint32_t kStageBytes = 3 * (kAPlane + kBPlane);
+constexpr int kStages = 3;
+constexpr int kAccs = 4;
+constexpr int kAccCols = kBN;
+constexpr int kTileRing = 8;
+constexpr int kChunksA = 128 * 8 / (32 * kConvWarps);        // 8-element chunks per thread
+constexpr int kChunksB = kBN / 2 * 8 / (32 * kConvWarps);
+
+struct Args {
+  TileShape shape;
+  WsHeader* hdr;
+  const float* a;      // W (y, dx) or x (dW)
+  const float* b;      // x, dy, dy
+  const float* bias;
+  float* out;
+  unsigned long long wait_ns;
+  int O, K;
+};
+
+// Eight consecutive floats, those from `n` on as zeros.
+template <bool kWide>
+__device__ __forceinline__ void load8(const float* p, int n, float (&v)[8]) {
+  if constexpr (kWide) {       // 16-byte aligned, n a multiple of 4
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
+    if (n > 0) a = __ldg(reinterpret_cast<const float4*>(p));
+    if (n > 4) b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+    v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = j < n ? __ldg(p + j) : 0.f;
+  }
+}
+
+// The three pieces of eight numbers, as 16 bytes each.  Rounding to 8 significant bits
+// adds half a unit to the magnitude and cuts; next to the largest number, where
+// that would overflow, hi is only cut.
+__device__ __forceinline__ void split8(const float (&v)[8], uint4& hi, uint4& mid, uint4& lo) {
+  uint32_t h[4], m[4], l[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t p[2], q[2];
+    float s[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const float x = v[2 * i + j], size = fabsf(x);
+      p[j] = __float_as_uint(x) + (size < 3e38f ? 0x8000u : 0u);
+      const float rest = x - __uint_as_float(p[j] & 0xffff0000u);
+      const float r = size < __int_as_float(0x7f800000) ? rest : 0.f;
+      q[j] = __float_as_uint(r) + 0x8000u;
+      s[j] = r - __uint_as_float(q[j] & 0xffff0000u);
+    }
+    h[i] = __byte_perm(p[0], p[1], 0x7632);
+    m[i] = __byte_perm(q[0], q[1], 0x7632);
+    l[i] = __byte_perm(__float_as_uint(s[0]), __float_as_uint(s[1]), 0x7632);
+  }
+  hi = make_uint4(h[0], h[1], h[2], h[3]);
+  mid = make_uint4(m[0], m[1], m[2], m[3]);
+  lo = make_uint4(l[0], l[1], l[2], l[3]);
+}
+
+template <int W, bool kWide>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+grouped_f32_kernel(const __grid_constant__ Args args) {
+  constexpr bool kAmn = W != kGroupedFwd, kBmn = W == kGroupedDw;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kStages * kStageBytes);
+  uint64_t* empty = full + kStages;
+  uint64_t* tfull = empty + kStages;
+  uint64_t* tempty = tfull + kAccs;
+  uint64_t* drain = tempty + kAccs;
+  uint64_t* ring_full = drain + 1;
+  uint64_t* ring_empty = ring_full + kTileRing;
+  Tile* ring = reinterpret_cast<Tile*>(ring_empty + kTileRing);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(ring + kTileRing);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  const bool leader = rank == 0;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      ptx::mbar_init(&full[s], 2 * kConvWarps);        // both CTAs' converter warps
+      ptx::mbar_init(&empty[s], 1);
+    }
+    for (int i = 0; i < kAccs; ++i) {
+      ptx::mbar_init(&tfull[i], 1);
+      ptx::mbar_init(&tempty[i], 2 * kSumWarps);
+    }
+    ptx::mbar_init(drain, 1);
+    for (int i = 0; i < kTileRing; ++i) {
+      ptx::mbar_init(&ring_full[i], 1);
+      ptx::mbar_init(&ring_empty[i], kSumWarps + kConvWarps + (leader ? 1 : 0));
+    }
+    *abort_flag = 0;
+    ptx::fence_mbar_init();
+  }
+  __syncthreads();
+  if (warp == 1) pair_tmem_alloc(tmem_slot, kAccs * kAccCols);
+  ptx::tc_fence_before();
+  cluster_sync();
+  ptx::tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  pdl_trigger();
+  pdl_wait();
+
+  const int total = W == kGroupedDw
+                        ? (args.hdr->err ? 0 : args.shape.N * args.shape.m_tiles * args.shape.n_tiles)
+                        : args.shape.prefix[args.shape.N] * args.shape.m_tiles;
+  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  auto fail = [&]() {
+    *abort_flag = 1;
+    atomicExch(&args.hdr->err, static_cast<int>(kDevPipelineTimeout));
+  };
+  // every lane of a warp leaves together
+  auto next_tile = [&](int i, Tile& ts) -> bool {
+    const int slot = i % kTileRing;
+    if (!__all_sync(0xffffffffu, ptx::mbar_wait(&ring_full[slot], (i / kTileRing) & 1, abort_flag,
+                                                args.wait_ns))) {
+      fail();
+      return false;
+    }
+    ts = ring[slot];
+    return ts.t >= 0;
+  };
+
+  if (warp == 2) {
+    // ------------------------------------------------------------ tile decoder
+    if (lane == 0) {
+      int t = pair;
+      for (int i = 0;; ++i, t += pairs) {
+        const int slot = i % kTileRing;
+        if (!ptx::mbar_wait(&ring_empty[slot], ((i / kTileRing) & 1) ^ 1u, abort_flag, args.wait_ns)) {
+          fail();
+          break;
+        }
+        const Tile ts = decode_tile<W>(t, total, args.shape);
+        ring[slot] = ts;
+        ptx::mbar_arrive(&ring_full[slot]);
+        if (ts.t < 0) break;
+      }
+    }
+    __syncwarp();
+  } else if (warp == 0) {
+    // ------------------------------------------------------------ MMA issuer
+    if (leader && lane == 0) {
+      int stage = 0, acc = 0;
+      uint32_t ph = 0, aph = 0;
+      bool ok = true;
+      for (int i = 0; ok; ++i) {
+        const int slot = i % kTileRing;
+        if (!ptx::mbar_wait(&ring_full[slot], (i / kTileRing) & 1, abort_flag, args.wait_ns)) {
+          fail();
+          break;
+        }
+        const Tile ts = ring[slot];
+        ptx::mbar_arrive(&ring_empty[slot]);
+        if (ts.t < 0) break;
+        const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | (kAmn ? 1u << 15 : 0u) |
+                               (kBmn ? 1u << 16 : 0u) | ((static_cast<uint32_t>(ts.n) >> 3) << 17) |
+                               ((256u >> 4) << 24);
+        for (int kb = 0; kb < ts.kb; ++kb) {
+          if (!cluster_bar_wait(&tempty[acc], aph ^ 1u, abort_flag, args.wait_ns) ||
+              !cluster_bar_wait(&full[stage], ph, abort_flag, args.wait_ns)) {
+            fail();
+            ok = false;
+            break;
+          }
+          ptx::tc_fence_after();
+          const uint32_t a = ptx::smem_u32(smem + stage * kStageBytes), b = a + 3 * kAPlane;
+          const uint32_t d = tmem + static_cast<uint32_t>(acc * kAccCols);
+          // pieces 0 hi, 1 mid, 2 lo; the small products first
+          constexpr int kPa[6] = {2, 0, 1, 1, 0, 0}, kPb[6] = {0, 2, 1, 0, 1, 0};
+#pragma unroll
+          for (int p = 0; p < 6; ++p)
+#pragma unroll
+            for (int k = 0; k < kBK / 16; ++k)
+              pair_mma(d, operand_desc<kAmn>(a + kPa[p] * kAPlane, k),
+                       operand_desc<kBmn>(b + kPb[p] * kBPlane, k), idesc, p != 0 || k != 0 ? 1u : 0u);
+          pair_commit(&empty[stage]);
+          pair_commit(&tfull[acc]);
+          if (++stage == kStages) {
+            stage = 0;
+            ph ^= 1u;
+          }
+          if (++acc == kAccs) {
+            acc = 0;
+            aph ^= 1u;
+          }
+        }
+      }
+      asm volatile(
+          "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+              ptx::smem_u32(drain))
+          : "memory");
+      volatile int never = 0;
+      if (!ptx::mbar_wait(drain, 0u, &never, args.wait_ns)) fail();
+    }
+    __syncwarp();
+  } else if (warp >= 4 + kSumWarps) {
+    // ------------------------------------------------------------ converters
+    const int tid = threadIdx.x - 32 * (4 + kSumWarps);
+    const uint32_t full0 = leader_addr(&full[0]);
+    int stage = 0;
+    uint32_t ph = 0;
+    bool ok = true;
+    for (int i = 0; ok; ++i) {
+      Tile ts;
+      if (!next_tile(i, ts)) break;
+      if (lane == 0) ptx::mbar_arrive(&ring_empty[i % kTileRing]);
+      const int half = ts.n >> 1;
+      const int m0 = ts.m0 + static_cast<int>(rank) * 128;
+      const int b0 = (W == kGroupedDw ? ts.n0 : ts.row0) + static_cast<int>(rank) * half;
+      // A chunk is 8 consecutive floats: of line (tid + 256 j) / 8, a 128-byte line of the
+      // bf16 tile.  K-major: line = row of the operand, the chunk along the depth;
+      // MN-major: line = depth within a box of 64 columns, the chunk along the columns.
+      // fetch returns the chunk's values for depth block kb (zeros outside).
+      auto fetch = [&](bool is_a, int j, int kb, float (&v)[8]) {
+        const int x = tid + 32 * kConvWarps * j, line = x >> 3, c = (x & 7) * 8;
+        const float* p;
+        int n;
+        if (is_a) {
+          if constexpr (W == kGroupedFwd) {            // W[e][m0 + line][kb 64 + c]
+            const int o = m0 + line, k = kb * kBK + c;
+            n = o < args.O ? args.K - k : 0;
+            p = args.a + (static_cast<int64_t>(ts.e) * args.O + o) * args.K + k;
+          } else if constexpr (W == kGroupedDx) {      // W[e][kb 64 + line % 64][m0 + ..]
+            const int o = kb * kBK + (line & 63), k = m0 + (line >> 6) * 64 + c;
+            n = o < args.O ? args.K - k : 0;
+            p = args.a + (static_cast<int64_t>(ts.e) * args.O + o) * args.K + k;
+          } else {                                     // x[row0 + kb 64 + line % 64][m0 + ..]
+            const int r = kb * kBK + (line & 63), k = m0 + (line >> 6) * 64 + c;
+            n = r < ts.rows ? args.K - k : 0;
+            p = args.a + (static_cast<int64_t>(ts.row0) + r) * args.K + k;
+          }
+        } else {
+          if constexpr (W == kGroupedDw) {             // dy[row0 + kb 64 + line][b0 + c]
+            const int r = kb * kBK + line, o = b0 + c;
+            n = r < ts.rows ? args.O - o : 0;
+            p = args.b + (static_cast<int64_t>(ts.row0) + r) * args.O + o;
+          } else {                                     // row b0 + line, depth kb 64 + c
+            const int depth = W == kGroupedFwd ? args.K : args.O;
+            const int k = kb * kBK + c;
+            n = line < half && b0 + line < ts.row0 + ts.rows ? depth - k : 0;
+            p = args.b + static_cast<int64_t>(b0 + line) * depth + k;
+          }
+        }
+        load8<kWide>(p, n, v);
+      };
+      auto put = [&](uint8_t* base, uint32_t plane, int j, const float (&v)[8]) {
+        const int x = tid + 32 * kConvWarps * j, line = x >> 3, c = x & 7;
+        uint8_t* at = base + line * 128 + ((c ^ (line & 7)) << 4);
+        uint4 hi, mid, lo;
+        split8(v, hi, mid, lo);
+        *reinterpret_cast<uint4*>(at) = hi;
+        *reinterpret_cast<uint4*>(at + plane) = mid;
+        *reinterpret_cast<uint4*>(at + 2 * plane) = lo;
+      };
+      // two sets of chunks: one is in flight while the other is split
+      constexpr int kSet = (kChunksA + kChunksB) / 2;
+      static_assert(kChunksA >= kSet && kChunksA + kChunksB == 2 * kSet, "chunk sets");
+      float v[2][kSet][8];
+      auto fetch_set = [&](int s, int kb) {
+#pragma unroll
+        for (int j = 0; j < kSet; ++j) {
+          const int q = s * kSet + j;
+          if (q < kChunksA) fetch(true, q, kb, v[s][j]);
+          else fetch(false, q - kChunksA, kb, v[s][j]);
+        }
+      };
+      if (ts.kb > 0) {
+        fetch_set(0, 0);
+        fetch_set(1, 0);
+      }
+      for (int kb = 0; kb < ts.kb; ++kb) {
+        if (!__all_sync(0xffffffffu, ptx::mbar_wait(&empty[stage], ph ^ 1u, abort_flag, args.wait_ns))) {
+          fail();
+          ok = false;
+          break;
+        }
+        uint8_t* a = smem + stage * kStageBytes;
+        uint8_t* b = a + 3 * kAPlane;
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+#pragma unroll
+          for (int j = 0; j < kSet; ++j) {
+            const int q = s * kSet + j;
+            if (q < kChunksA) put(a, kAPlane, q, v[s][j]);
+            else put(b, kBPlane, q - kChunksA, v[s][j]);
+          }
+          if (kb + 1 < ts.kb) fetch_set(s, kb + 1);
+        }
+        ptx::fence_proxy_async_smem();       // the stores, before the tensor cores' reads
+        __syncwarp();
+        if (lane == 0) arrive_at(full0 + stage * 8);
+        if (++stage == kStages) {
+          stage = 0;
+          ph ^= 1u;
+        }
+      }
+    }
+  } else if (warp >= 4) {
+    // ------------------------------------------------------------ sums and stores
+    const int q = warp & 3, side = (warp - 4) >> 2;
+    const uint32_t tempty0 = leader_addr(&tempty[0]);
+    int acc = 0;
+    uint32_t aph = 0;
+    bool ok = true;
+    for (int i = 0; ok; ++i) {
+      Tile ts;
+      if (!next_tile(i, ts)) break;
+      const int f = ts.m0 + static_cast<int>(rank) * 128 + q * 32 + lane;     // this lane's row of D
+      const int c0 = side * (kBN / 2);                                          // its 64 columns
+      float sum[kBN / 2];
+#pragma unroll
+      for (int j = 0; j < kBN / 2; ++j) sum[j] = 0.f;
+      for (int kb = 0; kb < ts.kb; ++kb) {
+        if (!__all_sync(0xffffffffu, ptx::mbar_wait(&tfull[acc], aph, abort_flag, args.wait_ns))) {
+          fail();
+          ok = false;
+          break;
+        }
+        ptx::tc_fence_after();
+        const uint32_t t0 = tmem + static_cast<uint32_t>(acc * kAccCols + c0) +
+                            (static_cast<uint32_t>(q * 32) << 16);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (c0 + h * 32 >= ts.n) break;
+          uint32_t r[32];
+          ptx::tmem_ld_32x32b_x32(t0 + h * 32, r);
+          ptx::tmem_ld_wait();
+#pragma unroll
+          for (int j = 0; j < 32; ++j) sum[h * 32 + j] += __uint_as_float(r[j]);
+        }
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_at(tempty0 + acc * 8);
+        if (++acc == kAccs) {
+          acc = 0;
+          aph ^= 1u;
+        }
+      }
+      if (!ok) break;
+      if constexpr (W == kGroupedDw) {
+        // lane = column k of dW[e], its 64 sums = rows o
+        const int n = args.O - ts.n0 - c0;
+        if (f < args.K) {
+          float* o = args.out + (static_cast<int64_t>(ts.e) * args.O + ts.n0 + c0) * args.K + f;
+#pragma unroll
+          for (int j = 0; j < kBN / 2; ++j)
+            if (j < n) o[static_cast<int64_t>(j) * args.K] = sum[j];
+        }
+      } else {
+        const int m = W == kGroupedFwd ? args.O : args.K;
+        const int n = ts.rows - c0;
+        if (f < m) {
+          float bias = 0.f;
+          if (W == kGroupedFwd && args.bias) bias = args.bias[static_cast<int64_t>(ts.e) * m + f];
+          float* o = args.out + (static_cast<int64_t>(ts.row0) + c0) * m + f;
+#pragma unroll
+          for (int j = 0; j < kBN / 2; ++j)
+            if (j < n) o[static_cast<int64_t>(j) * m] = sum[j] + bias;
+        }
+      }
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(&ring_empty[i % kTileRing]);
+    }
+  }
+  __syncwarp();
+  ptx::tc_fence_before();
+  cluster_sync();
+  if (warp == 1) {
+    ptx::tc_fence_after();
+    pair_tmem_dealloc(tmem, kAccs * kAccCols);
+  }
+}
+
+}  // namespace
+
+int grouped_f32_tile_rows() { return kBN; }
+
+cudaError_t launch_grouped_f32(const GroupedShape& s, const GroupedPlan& p, GroupedWhich which,
+                               const int* offsets, const void* a, const void* b, const void* bias,
+                               void* out, int num_sms, cudaStream_t stream) {
+  Args g = {};
+  const bool dw = which == kGroupedDw;
+  // callers give (x, W), (dy, W) and (dy, x)
+  g.a = static_cast<const float*>(b);
+  g.b = static_cast<const float*>(a);
+  g.bias = static_cast<const float*>(bias);
+  g.out = static_cast<float*>(out);
+  g.hdr = p.hdr;
+  g.wait_ns = wait_limit_ns();
+  g.O = static_cast<int>(s.O);
+  g.K = static_cast<int>(s.K);
+  g.shape.off = offsets;
+  g.shape.prefix = p.tile_prefix;
+  g.shape.N = static_cast<int>(s.N);
+  const int64_t m = which == kGroupedFwd ? s.O : s.K, depth = which == kGroupedFwd ? s.K : s.O;
+  g.shape.m_tiles = static_cast<int>((m + 255) / 256);
+  g.shape.n_tiles = static_cast<int>((s.O + kBN - 1) / kBN);
+  g.shape.cols = g.O;
+  g.shape.bn_cols = kBN;
+  g.shape.k_blocks = static_cast<int>((depth + kBK - 1) / kBK);
+  const int64_t tiles = dw ? s.N * g.shape.m_tiles * g.shape.n_tiles
+                           : (s.R / kBN + s.N) * g.shape.m_tiles;      // at most
+  // 16-byte loads when every row of both operands starts on a 16-byte boundary
+  auto aligned = [](const void* q) { return (reinterpret_cast<uintptr_t>(q) & 15) == 0; };
+  const bool wide = aligned(a) && aligned(b) && s.K % 4 == 0 && s.O % 4 == 0;
+  auto* kernel = which == kGroupedFwd  ? (wide ? grouped_f32_kernel<kGroupedFwd, true>
+                                               : grouped_f32_kernel<kGroupedFwd, false>)
+                 : which == kGroupedDx ? (wide ? grouped_f32_kernel<kGroupedDx, true>
+                                               : grouped_f32_kernel<kGroupedDx, false>)
+                                       : (wide ? grouped_f32_kernel<kGroupedDw, true>
+                                               : grouped_f32_kernel<kGroupedDw, false>);
+  const size_t smem = 1024 + kStages * kStageBytes + (2 * kStages + 2 * kAccs + 1 + 2 * kTileRing) * 8 +
+                      kTileRing * sizeof(Tile) + 64;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
+  const int64_t pairs = num_sms / 2;
+  count_launch();
+  return launch_dependent(kernel, dim3(static_cast<unsigned>(2 * (tiles < pairs ? tiles : pairs))),
+                          dim3(kThreads), smem, stream, g);
+}
+
+}  // namespace swl

@@ -30,21 +30,18 @@
 #include <cuda_runtime.h>
 
 #include "grouped_products.h"
-#include "sm100_ptx.cuh"
+#include "grouped_sm100.cuh"
 
 namespace swl {
 namespace {
 
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 128 + 32 * kEpiWarps;
-constexpr int kBK = 64;                          // depth of a stage (128 bytes of bf16)
 constexpr uint32_t kABytes = 128 * kBK * 2;      // a CTA's half of A
 constexpr int kMaxStages = 12;
 constexpr int kAccs = 2;
 constexpr int kTmemCols = 512;
 constexpr int kTileRing = 8;
-constexpr int kBand = 8;                         // row tiles of a band (2048 rows)
-constexpr int kUnit = 32;                        // rows a tile's n grows by
 // Staging of an epilogue warp: y, dx: 32 rows of 32 features; dW: 32 rows of 64 columns,
 // twice (the next rows are converted while a store reads the last ones).
 template <int W>
@@ -54,18 +51,13 @@ constexpr int epi_bytes() {
 constexpr size_t kSmemLimit = 227 * 1024;
 
 struct Args {
-  const int* off;
-  const int* prefix;
+  TileShape shape;
   WsHeader* hdr;
   const CUtensorMap* maps;      // dW: [2 N] maps of dy and x per group
   const __nv_bfloat16* bias;
   __nv_bfloat16* out;
   unsigned long long wait_ns;
-  int N;
   int m;           // rows of D per group: O (y, dW) or K (dx); the epilogue's features
-  int cols;        // dW: columns of D (K)
-  int k_blocks;    // y, dx: ceil(depth / 64)
-  int m_tiles, n_tiles;   // n_tiles: dW only
   int bn;          // most rows of B per tile
   int stages;
   int keep_w;      // W is read by several row tiles: no evict-first
@@ -79,98 +71,6 @@ struct RowMaps {
   CUtensorMap box[kBoxes];
 };
 
-struct Tile {
-  int t;           // -1: no more
-  int e, m0, row0, rows, n, n0, kb;
-};
-
-// ---------------------------------------------------------------- pair PTX
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
-                   : "memory");
-}
-// Address of the first CTA's copy of a shared variable.
-__device__ __forceinline__ uint32_t leader_addr(const void* p) {
-  uint32_t a;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(ptx::smem_u32(p)));
-  return a;
-}
-__device__ __forceinline__ void arrive_at(uint32_t cluster_bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar)
-               : "memory");
-}
-__device__ __forceinline__ void pair_tmem_alloc(uint32_t* dst, uint32_t cols) {
-  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
-                   ptx::smem_u32(dst)),
-               "r"(cols)
-               : "memory");
-  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void pair_tmem_dealloc(uint32_t addr, uint32_t cols) {
-  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols)
-               : "memory");
-}
-__device__ __forceinline__ void pair_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                         uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-// Arrive on both CTAs' copies of `bar` once this thread's products have finished.
-__device__ __forceinline__ void pair_commit(uint64_t* bar) {
-  const uint16_t both = 3;
-  asm volatile(
-      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
-      "[%0], %1;" ::"r"(ptx::smem_u32(bar)),
-      "h"(both)
-      : "memory");
-}
-// TMA loads into this CTA's shared memory that complete on the first CTA's barrier.
-__device__ __forceinline__ void pair_load_2d(void* dst, const CUtensorMap* map, uint32_t bar,
-                                             int c0, int c1, uint64_t policy) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
-      ".L2::cache_hint [%0], [%1, {%3, %4}], [%2], %5;" ::"r"(ptx::smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "l"(policy)
-      : "memory");
-}
-__device__ __forceinline__ void pair_load_3d(void* dst, const CUtensorMap* map, uint32_t bar,
-                                             int c0, int c1, int c2, uint64_t policy) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
-      ".L2::cache_hint [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(ptx::smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "l"(policy)
-      : "memory");
-}
-__device__ __forceinline__ uint64_t l2_policy_normal() {
-  uint64_t p;
-  asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
-  return p;
-}
-// MN-major bf16 tile in 128-byte-swizzled boxes of [64 k][64 mn]: 8-row groups along
-// k 1024 bytes apart (stride offset), boxes along mn 8192 bytes apart (leading offset).
-__device__ __forceinline__ uint64_t desc_mn_major(uint32_t addr) {
-  uint64_t d = 0;
-  d |= static_cast<uint64_t>((addr >> 4) & 0x3FFFu);
-  d |= static_cast<uint64_t>(8192u >> 4) << 16;
-  d |= static_cast<uint64_t>(1024u >> 4) << 32;
-  d |= static_cast<uint64_t>(1u) << 46;
-  d |= static_cast<uint64_t>(2u) << 61;
-  return d;
-}
-template <bool kMn>
-__device__ __forceinline__ uint64_t operand_desc(uint32_t base, int k) {
-  // 16 deep: 32 bytes along a K-major row, or 16 rows of 128 bytes
-  return kMn ? desc_mn_major(base + k * 2048) : ptx::umma_desc_sw128_kmajor(base + k * 32);
-}
 
 // ---------------------------------------------------------------- the kernel
 template <int W>
@@ -231,8 +131,8 @@ grouped_sm100_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
   pdl_trigger();
   pdl_wait();
 
-  const int total = W == kGroupedDw ? (args.hdr->err ? 0 : args.N * args.m_tiles * args.n_tiles)
-                                    : args.prefix[args.N] * args.m_tiles;
+  const int total = W == kGroupedDw ? (args.hdr->err ? 0 : args.shape.N * args.shape.m_tiles * args.shape.n_tiles)
+                                    : args.shape.prefix[args.shape.N] * args.shape.m_tiles;
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   auto fail = [&]() {
     *abort_flag = 1;
@@ -249,49 +149,7 @@ grouped_sm100_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
           fail();
           break;
         }
-        Tile ts = {};
-        ts.t = t < total ? t : -1;
-        if (ts.t >= 0) {
-          if constexpr (W == kGroupedDw) {
-            const int per = args.m_tiles * args.n_tiles;
-            ts.e = t / per;
-            const int r = t - ts.e * per;
-            ts.m0 = r / args.n_tiles * 256;
-            ts.n0 = (r % args.n_tiles) * 256;
-            ts.row0 = __ldg(args.off + ts.e);
-            ts.rows = __ldg(args.off + ts.e + 1) - ts.row0;
-            ts.n = min(256, (args.cols - ts.n0 + 127) & ~127);
-            ts.kb = (ts.rows + kBK - 1) / kBK;
-          } else {
-            const int q = t / args.m_tiles;
-            int lo = 0, hi = args.N;
-            while (hi - lo > 1) {
-              const int mid = (lo + hi) >> 1;
-              if (__ldg(args.prefix + mid) <= q) lo = mid;
-              else hi = mid;
-            }
-            const int p0 = __ldg(args.prefix + lo), nts = __ldg(args.prefix + lo + 1) - p0;
-            // bands of kBand row tiles go through all of W, row tiles fastest: the tiles
-            // running together share few rows of x and few of W
-            const int local = t - p0 * args.m_tiles;
-            const int band = local / (kBand * args.m_tiles);
-            const int r = local - band * kBand * args.m_tiles;
-            const int in_band = min(kBand, nts - band * kBand);
-            const int nt = band * kBand + r % in_band;
-            ts.e = lo;
-            ts.m0 = r / in_band * 256;
-            // the group's rows in nts parts of whole units, as even as they go: no short
-            // tile that loads as much W as a full one
-            const int begin = __ldg(args.off + lo), rows = __ldg(args.off + lo + 1) - begin;
-            const int units = (rows + kUnit - 1) / kUnit;
-            const int per = units / nts, more = units - per * nts;
-            const int first = (nt * per + min(nt, more)) * kUnit;
-            ts.row0 = begin + first;
-            ts.n = (per + (nt < more ? 1 : 0)) * kUnit;
-            ts.rows = min(ts.n, rows - first);
-            ts.kb = args.k_blocks;
-          }
-        }
+        const Tile ts = decode_tile<W>(t, total, args.shape);
         ring[slot] = ts;
         ptx::mbar_arrive(&ring_full[slot]);
         if (ts.t < 0) break;
@@ -389,7 +247,7 @@ grouped_sm100_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
         ptx::mbar_arrive(&ring_empty[slot]);
         if (ts.t < 0) break;
         if (ts.kb == 0) continue;
-        if (!ptx::mbar_wait(&tempty[acc], aph ^ 1u, abort_flag, args.wait_ns)) {
+        if (!cluster_bar_wait(&tempty[acc], aph ^ 1u, abort_flag, args.wait_ns)) {
           fail();
           break;
         }
@@ -469,7 +327,7 @@ grouped_sm100_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
         // 64 columns at a time: a lane converts its row, the rows go out by a TMA store
         // from 128-byte-swizzled staging (whole 128-byte lines; rows and columns past the
         // end of the group's matrix are not written)
-        const int width = min(ts.n, args.cols - ts.n0);
+        const int width = min(ts.n, args.shape.cols - ts.n0);
         for (int c0 = side * 64; c0 < width; c0 += 128) {
           uint32_t r[2][32];
           if (ts.kb > 0) {
@@ -575,25 +433,26 @@ cudaError_t launch_grouped_sm100(const GroupedShape& s, const GroupedPlan& p, Gr
   CUtensorMap mapA = {}, mapOut = {};
   RowMaps rows = {};
   Args g = {};
-  g.off = offsets;
-  g.prefix = p.tile_prefix;
+  g.shape.off = offsets;
+  g.shape.prefix = p.tile_prefix;
   g.hdr = p.hdr;
   g.maps = static_cast<const CUtensorMap*>(p.maps);
   g.bias = static_cast<const __nv_bfloat16*>(bias);
   g.out = static_cast<__nv_bfloat16*>(out);
   g.wait_ns = wait_limit_ns();
-  g.N = static_cast<int>(N);
+  g.shape.N = static_cast<int>(N);
   int64_t tiles;      // at most
   if (which == kGroupedDw) {
     const uint64_t dout[3] = {K, O, N};
     const uint32_t bout[3] = {64, 32, 1};
     if (!encode_tmap_bf16(&mapOut, out, 3, dout, bout)) return cudaErrorInvalidValue;
     g.m = static_cast<int>(O);
-    g.cols = static_cast<int>(K);
-    g.n_tiles = static_cast<int>((K + 255) / 256);
+    g.shape.cols = static_cast<int>(K);
+    g.shape.n_tiles = static_cast<int>((K + 255) / 256);
+    g.shape.bn_cols = 256;
     g.bn = K <= 128 ? 128 : 256;
-    g.m_tiles = (g.m + 255) / 256;
-    tiles = static_cast<int64_t>(N) * g.m_tiles * g.n_tiles;
+    g.shape.m_tiles = (g.m + 255) / 256;
+    tiles = static_cast<int64_t>(N) * g.shape.m_tiles * g.shape.n_tiles;
   } else {
     const uint64_t dw[3] = {K, O, N}, dr[2] = {which == kGroupedFwd ? K : O, R};
     const uint32_t bw[3] = {64, which == kGroupedFwd ? 128u : 64u, 1};
@@ -605,10 +464,10 @@ cudaError_t launch_grouped_sm100(const GroupedShape& s, const GroupedPlan& p, Gr
       if (!encode_tmap_bf16(&rows.box[i], a, 2, dr, br)) return cudaErrorInvalidValue;
     }
     g.m = static_cast<int>(which == kGroupedFwd ? O : K);
-    g.k_blocks = static_cast<int>((dr[0] + kBK - 1) / kBK);
-    g.m_tiles = (g.m + 255) / 256;
+    g.shape.k_blocks = static_cast<int>((dr[0] + kBK - 1) / kBK);
+    g.shape.m_tiles = (g.m + 255) / 256;
     g.keep_w = s.R > 2 * g.bn * s.N;
-    tiles = (s.R / g.bn + s.N) * g.m_tiles;
+    tiles = (s.R / g.bn + s.N) * g.shape.m_tiles;
   }
   const size_t stage = kABytes + static_cast<size_t>(g.bn / 2) * kBK * 2;
   const size_t fixed = 1024 + (which == kGroupedDw ? epi_bytes<kGroupedDw>() : epi_bytes<kGroupedFwd>()) + (2 * kMaxStages + 2 * kAccs + 1 + 2 * kTileRing) * 8 +

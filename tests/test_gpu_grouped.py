@@ -2,8 +2,9 @@
 
 Tolerance: a sum of n products of exact factors in fp32, every partial sum off by at
 most 2^-23 of the sum S of the absolute products (rounded or truncated), is off by at
-most (n + 2) 2^-23 S; then half a step of the output type.  A split of an fp32 factor
-into pieces that are exact to 2^-24 adds 4 2^-24 S.
+most (n + 2) 2^-23 S; then half a step of the output type.  The products that stand
+for one of two fp32 numbers leave out at most 2^-23 of it, another 2^-23 S (and the
+squares of these, well under a fourth).
 """
 from __future__ import annotations
 
