@@ -24,8 +24,8 @@
 // products of a 64-deep step take 1536 cycles and its 12288 elements about 900 issue
 // cycles, for fewer rows the loads bound it.
 //
-// Roles of a CTA's 20 warps: 0 MMA issuer (first CTA only), 1 TMEM, 2 tile decoder,
-// 4-11 sums and stores (two warps per lane quarter), 12-19 converters.
+// Roles of a CTA's 20 warps: 0 MMA issuer (first CTA only), 1 TMEM, 2 tile decoder, 3
+// relay between the converters and the first CTA, 4-11 sums and stores (two warps per lane quarter), 12-19 converters.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -45,8 +45,6 @@ constexpr int kStages = 3;
 constexpr int kAccs = 4;
 constexpr int kAccCols = kBN;
 constexpr int kTileRing = 8;
-constexpr int kChunksA = 128 * 8 / (32 * kConvWarps);        // 8-element chunks per thread
-constexpr int kChunksB = kBN / 2 * 8 / (32 * kConvWarps);
 
 struct Args {
   TileShape shape;
@@ -57,49 +55,99 @@ struct Args {
   float* out;
   unsigned long long wait_ns;
   int O, K;
+  bool even_a, even_b;   // every row of the operand starts on an 8-byte boundary
 };
 
-// Eight consecutive floats, those from `n` on as zeros.
+// The three pieces of two numbers, packed.  Rounding to 8 significant bits adds half a
+// unit to the magnitude and cuts; next to the largest number, where that would
+// overflow, hi is only cut.
+__device__ __forceinline__ void split2(float x0, float x1, uint32_t& hi, uint32_t& mid,
+                                       uint32_t& lo) {
+  const float x[2] = {x0, x1};
+  uint32_t p[2], q[2];
+  float s[2];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const float size = fabsf(x[j]);
+    p[j] = __float_as_uint(x[j]) + (size < 3e38f ? 0x8000u : 0u);
+    const float rest = x[j] - __uint_as_float(p[j] & 0xffff0000u);
+    const float r = size < __int_as_float(0x7f800000) ? rest : 0.f;
+    q[j] = __float_as_uint(r) + 0x8000u;
+    s[j] = r - __uint_as_float(q[j] & 0xffff0000u);
+  }
+  hi = __byte_perm(p[0], p[1], 0x7632);
+  mid = __byte_perm(q[0], q[1], 0x7632);
+  lo = __byte_perm(__float_as_uint(s[0]), __float_as_uint(s[1]), 0x7632);
+}
+
+// What a converting thread holds of a stage: kCount runs of kRun consecutive floats of
+// the operands' lines.  kWide (every row of both operands on a 16-byte boundary): runs
+// of 8, two 16-byte loads each, a line taken by 8 threads.  Else runs of 2, a line taken
+// by a whole warp, so that its loads stay within the line's sectors (8 floats per thread
+// by single loads touch every sector 8 times): one 8-byte load when the operand's rows
+// all start on one, else two loads.
 template <bool kWide>
-__device__ __forceinline__ void load8(const float* p, int n, float (&v)[8]) {
-  if constexpr (kWide) {       // 16-byte aligned, n a multiple of 4
+struct Runs {
+  static constexpr int kRun = kWide ? 8 : 2;
+  static constexpr int kPerLine = kBK / kRun;
+  static constexpr int kLines = 32 * kConvWarps / kPerLine;      // lines a round takes
+  static constexpr int kA = 128 / kLines, kB = kBN / 2 / kLines;   // rounds of A and of B
+  static constexpr int kSet = (kA + kB) / 2;
+  static_assert(kA >= kSet && kA + kB == 2 * kSet, "two sets, the first of A alone");
+  float v[2][kSet][kRun];
+};
+template <bool kWide>
+__device__ __forceinline__ void load_run(const float* p, int n, bool even,
+                                         float (&v)[Runs<kWide>::kRun]) {
+  if constexpr (kWide) {       // n is a multiple of 4
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
     if (n > 0) a = __ldg(reinterpret_cast<const float4*>(p));
     if (n > 4) b = __ldg(reinterpret_cast<const float4*>(p) + 1);
     v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
     v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  } else if (even) {           // n is even
+    float2 a = make_float2(0.f, 0.f);
+    if (n > 0) a = __ldg(reinterpret_cast<const float2*>(p));
+    v[0] = a.x, v[1] = a.y;
   } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = j < n ? __ldg(p + j) : 0.f;
+    v[0] = n > 0 ? __ldg(p) : 0.f;
+    v[1] = n > 1 ? __ldg(p + 1) : 0.f;
   }
 }
 
-// The three pieces of eight numbers, as 16 bytes each.  Rounding to 8 significant bits
-// adds half a unit to the magnitude and cuts; next to the largest number, where
-// that would overflow, hi is only cut.
-__device__ __forceinline__ void split8(const float (&v)[8], uint4& hi, uint4& mid, uint4& lo) {
-  uint32_t h[4], m[4], l[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    uint32_t p[2], q[2];
-    float s[2];
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const float x = v[2 * i + j], size = fabsf(x);
-      p[j] = __float_as_uint(x) + (size < 3e38f ? 0x8000u : 0u);
-      const float rest = x - __uint_as_float(p[j] & 0xffff0000u);
-      const float r = size < __int_as_float(0x7f800000) ? rest : 0.f;
-      q[j] = __float_as_uint(r) + 0x8000u;
-      s[j] = r - __uint_as_float(q[j] & 0xffff0000u);
-    }
-    h[i] = __byte_perm(p[0], p[1], 0x7632);
-    m[i] = __byte_perm(q[0], q[1], 0x7632);
-    l[i] = __byte_perm(__float_as_uint(s[0]), __float_as_uint(s[1]), 0x7632);
+// One operand of a tile as a converting thread walks it.  A line is 64 consecutive
+// floats, 128 bytes of each of the bf16 tiles.  K-major: a line is a row of the operand
+// and runs along the depth, its next depth block is 64 floats on; MN-major: a line is
+// a depth and runs along 64 of the operand's rows (lines 64 on: the next 64 rows), the
+// next depth block is 64 lines on.
+template <bool kMn>
+struct Side {
+  const float* p;    // this thread's element of line line0, this depth block
+  int64_t ld;
+  int lines;         // lines that are there, of this depth block on (K-major: of the tile)
+  int n;             // elements that are there from p on
+  __device__ __forceinline__ void start(const float* base, int64_t stride, int there, int width,
+                                        int line0, int c) {
+    p = base + line0 * stride + c;
+    ld = stride;
+    lines = there;
+    n = width - c;
   }
-  hi = make_uint4(h[0], h[1], h[2], h[3]);
-  mid = make_uint4(m[0], m[1], m[2], m[3]);
-  lo = make_uint4(l[0], l[1], l[2], l[3]);
-}
+  __device__ __forceinline__ void next() {
+    p += kMn ? kBK * ld : kBK;
+    if (kMn) lines -= kBK;
+    else n -= kBK;
+  }
+  // Round j's run: line line0 + kLines j.
+  template <bool kWide>
+  __device__ __forceinline__ void load(int j, int line0, bool even,
+                                       float (&v)[Runs<kWide>::kRun]) const {
+    const int first = Runs<kWide>::kLines * j;
+    const int line = kMn ? first & 63 : first, box = kMn ? first >> 6 : 0;
+    const int there = line0 + line < lines ? n - box * 64 : 0;
+    load_run<kWide>(p + line * ld + box * 64, there, even, v);
+  }
+};
 
 template <int W, bool kWide>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
@@ -109,7 +157,8 @@ grouped_f32_kernel(const __grid_constant__ Args args) {
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + kStages * kStageBytes);
-  uint64_t* empty = full + kStages;
+  uint64_t* mine = full + kStages;        // this CTA's half of a stage is there
+  uint64_t* empty = mine + kStages;
   uint64_t* tfull = empty + kStages;
   uint64_t* tempty = tfull + kAccs;
   uint64_t* drain = tempty + kAccs;
@@ -124,7 +173,8 @@ grouped_f32_kernel(const __grid_constant__ Args args) {
   const bool leader = rank == 0;
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
-      ptx::mbar_init(&full[s], 2 * kConvWarps);        // both CTAs' converter warps
+      ptx::mbar_init(&full[s], 2);                 // both CTAs' halves
+      ptx::mbar_init(&mine[s], kConvWarps);
       ptx::mbar_init(&empty[s], 1);
     }
     for (int i = 0; i < kAccs; ++i) {
@@ -134,7 +184,7 @@ grouped_f32_kernel(const __grid_constant__ Args args) {
     ptx::mbar_init(drain, 1);
     for (int i = 0; i < kTileRing; ++i) {
       ptx::mbar_init(&ring_full[i], 1);
-      ptx::mbar_init(&ring_empty[i], kSumWarps + kConvWarps + (leader ? 1 : 0));
+      ptx::mbar_init(&ring_empty[i], kSumWarps + kConvWarps + 1 + (leader ? 1 : 0));
     }
     *abort_flag = 0;
     ptx::fence_mbar_init();
@@ -241,10 +291,42 @@ grouped_f32_kernel(const __grid_constant__ Args args) {
       if (!ptx::mbar_wait(drain, 0u, &never, args.wait_ns)) fail();
     }
     __syncwarp();
+  } else if (warp == 3) {
+    // ------------------------------------------------------------ relay
+    // Tells the first CTA of this CTA's halves, one release at cluster scope for all
+    // converter warps.
+    if (lane == 0) {
+      const uint32_t full0 = leader_addr(&full[0]);
+      int stage = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      for (int i = 0; ok; ++i) {
+        const int slot = i % kTileRing;
+        if (!ptx::mbar_wait(&ring_full[slot], (i / kTileRing) & 1, abort_flag, args.wait_ns)) {
+          fail();
+          break;
+        }
+        const Tile ts = ring[slot];
+        ptx::mbar_arrive(&ring_empty[slot]);
+        if (ts.t < 0) break;
+        for (int kb = 0; kb < ts.kb; ++kb) {
+          if (!ptx::mbar_wait(&mine[stage], ph, abort_flag, args.wait_ns)) {
+            fail();
+            ok = false;
+            break;
+          }
+          arrive_at(full0 + stage * 8);
+          if (++stage == kStages) {
+            stage = 0;
+            ph ^= 1u;
+          }
+        }
+      }
+    }
+    __syncwarp();
   } else if (warp >= 4 + kSumWarps) {
     // ------------------------------------------------------------ converters
     const int tid = threadIdx.x - 32 * (4 + kSumWarps);
-    const uint32_t full0 = leader_addr(&full[0]);
     int stage = 0;
     uint32_t ph = 0;
     bool ok = true;
@@ -254,67 +336,62 @@ grouped_f32_kernel(const __grid_constant__ Args args) {
       if (lane == 0) ptx::mbar_arrive(&ring_empty[i % kTileRing]);
       const int half = ts.n >> 1;
       const int m0 = ts.m0 + static_cast<int>(rank) * 128;
-      const int b0 = (W == kGroupedDw ? ts.n0 : ts.row0) + static_cast<int>(rank) * half;
-      // A chunk is 8 consecutive floats: of line (tid + 256 j) / 8, a 128-byte line of the
-      // bf16 tile.  K-major: line = row of the operand, the chunk along the depth;
-      // MN-major: line = depth within a box of 64 columns, the chunk along the columns.
-      // fetch returns the chunk's values for depth block kb (zeros outside).
-      auto fetch = [&](bool is_a, int j, int kb, float (&v)[8]) {
-        const int x = tid + 32 * kConvWarps * j, line = x >> 3, c = (x & 7) * 8;
-        const float* p;
-        int n;
-        if (is_a) {
-          if constexpr (W == kGroupedFwd) {            // W[e][m0 + line][kb 64 + c]
-            const int o = m0 + line, k = kb * kBK + c;
-            n = o < args.O ? args.K - k : 0;
-            p = args.a + (static_cast<int64_t>(ts.e) * args.O + o) * args.K + k;
-          } else if constexpr (W == kGroupedDx) {      // W[e][kb 64 + line % 64][m0 + ..]
-            const int o = kb * kBK + (line & 63), k = m0 + (line >> 6) * 64 + c;
-            n = o < args.O ? args.K - k : 0;
-            p = args.a + (static_cast<int64_t>(ts.e) * args.O + o) * args.K + k;
-          } else {                                     // x[row0 + kb 64 + line % 64][m0 + ..]
-            const int r = kb * kBK + (line & 63), k = m0 + (line >> 6) * 64 + c;
-            n = r < ts.rows ? args.K - k : 0;
-            p = args.a + (static_cast<int64_t>(ts.row0) + r) * args.K + k;
-          }
-        } else {
-          if constexpr (W == kGroupedDw) {             // dy[row0 + kb 64 + line][b0 + c]
-            const int r = kb * kBK + line, o = b0 + c;
-            n = r < ts.rows ? args.O - o : 0;
-            p = args.b + (static_cast<int64_t>(ts.row0) + r) * args.O + o;
-          } else {                                     // row b0 + line, depth kb 64 + c
-            const int depth = W == kGroupedFwd ? args.K : args.O;
-            const int k = kb * kBK + c;
-            n = line < half && b0 + line < ts.row0 + ts.rows ? depth - k : 0;
-            p = args.b + static_cast<int64_t>(b0 + line) * depth + k;
-          }
-        }
-        load8<kWide>(p, n, v);
-      };
-      auto put = [&](uint8_t* base, uint32_t plane, int j, const float (&v)[8]) {
-        const int x = tid + 32 * kConvWarps * j, line = x >> 3, c = x & 7;
-        uint8_t* at = base + line * 128 + ((c ^ (line & 7)) << 4);
-        uint4 hi, mid, lo;
-        split8(v, hi, mid, lo);
-        *reinterpret_cast<uint4*>(at) = hi;
-        *reinterpret_cast<uint4*>(at + plane) = mid;
-        *reinterpret_cast<uint4*>(at + 2 * plane) = lo;
-      };
-      // two sets of chunks: one is in flight while the other is split
-      constexpr int kSet = (kChunksA + kChunksB) / 2;
-      static_assert(kChunksA >= kSet && kChunksA + kChunksB == 2 * kSet, "chunk sets");
-      float v[2][kSet][8];
-      auto fetch_set = [&](int s, int kb) {
+      const int b0 = static_cast<int>(rank) * half;
+      using R = Runs<kWide>;
+      const int line0 = tid / R::kPerLine, c = (tid % R::kPerLine) * R::kRun;
+      Side<kAmn> A;
+      Side<kBmn> B;
+      if constexpr (W == kGroupedFwd) {
+        A.start(args.a + (static_cast<int64_t>(ts.e) * args.O + m0) * args.K, args.K, args.O - m0,
+                args.K, line0, c);
+        B.start(args.b + (static_cast<int64_t>(ts.row0) + b0) * args.K, args.K,
+                min(half, ts.rows - b0), args.K, line0, c);
+      } else if constexpr (W == kGroupedDx) {
+        A.start(args.a + static_cast<int64_t>(ts.e) * args.O * args.K + m0, args.K, args.O,
+                args.K - m0, line0, c);
+        B.start(args.b + (static_cast<int64_t>(ts.row0) + b0) * args.O, args.O,
+                min(half, ts.rows - b0), args.O, line0, c);
+      } else {
+        A.start(args.a + static_cast<int64_t>(ts.row0) * args.K + m0, args.K, ts.rows, args.K - m0,
+                line0, c);
+        B.start(args.b + static_cast<int64_t>(ts.row0) * args.O + ts.n0 + b0, args.O, ts.rows,
+                args.O - ts.n0 - b0, line0, c);
+      }
+      R runs;
+      // two sets: one is in flight while the other is split
+      auto fetch_set = [&](int s) {
 #pragma unroll
-        for (int j = 0; j < kSet; ++j) {
-          const int q = s * kSet + j;
-          if (q < kChunksA) fetch(true, q, kb, v[s][j]);
-          else fetch(false, q - kChunksA, kb, v[s][j]);
+        for (int j = 0; j < R::kSet; ++j) {
+          const int q = s * R::kSet + j;
+          if (q < R::kA) A.template load<kWide>(q, line0, args.even_a, runs.v[s][j]);
+          else B.template load<kWide>(q - R::kA, line0, args.even_b, runs.v[s][j]);
+        }
+      };
+      const uint32_t at0 = line0 * 128 + (((c >> 3) ^ (line0 & 7)) << 4) + (c & 7) * 2;
+      auto put_set = [&](int s, uint8_t* a) {
+#pragma unroll
+        for (int j = 0; j < R::kSet; ++j) {
+          const int q = s * R::kSet + j;
+          const uint32_t plane = q < R::kA ? kAPlane : kBPlane;
+          // (rounds are whole multiples of 8 lines: the swizzle stays)
+          uint8_t* at = a + at0 + (q < R::kA ? q * R::kLines * 128
+                                             : 3 * kAPlane + (q - R::kA) * R::kLines * 128);
+          uint32_t w[3][R::kRun / 2];
+#pragma unroll
+          for (int i = 0; i < R::kRun / 2; ++i)
+            split2(runs.v[s][j][2 * i], runs.v[s][j][2 * i + 1], w[0][i], w[1][i], w[2][i]);
+#pragma unroll
+          for (int i = 0; i < 3; ++i) {
+            if constexpr (kWide)
+              *reinterpret_cast<uint4*>(at + i * plane) = make_uint4(w[i][0], w[i][1], w[i][2], w[i][3]);
+            else
+              *reinterpret_cast<uint32_t*>(at + i * plane) = w[i][0];
+          }
         }
       };
       if (ts.kb > 0) {
-        fetch_set(0, 0);
-        fetch_set(1, 0);
+        fetch_set(0);
+        fetch_set(1);
       }
       for (int kb = 0; kb < ts.kb; ++kb) {
         if (!__all_sync(0xffffffffu, ptx::mbar_wait(&empty[stage], ph ^ 1u, abort_flag, args.wait_ns))) {
@@ -323,20 +400,18 @@ grouped_f32_kernel(const __grid_constant__ Args args) {
           break;
         }
         uint8_t* a = smem + stage * kStageBytes;
-        uint8_t* b = a + 3 * kAPlane;
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-#pragma unroll
-          for (int j = 0; j < kSet; ++j) {
-            const int q = s * kSet + j;
-            if (q < kChunksA) put(a, kAPlane, q, v[s][j]);
-            else put(b, kBPlane, q - kChunksA, v[s][j]);
+          if (s == 0) {
+            A.next();
+            B.next();
           }
-          if (kb + 1 < ts.kb) fetch_set(s, kb + 1);
+          put_set(s, a);
+          if (kb + 1 < ts.kb) fetch_set(s);
         }
         ptx::fence_proxy_async_smem();       // the stores, before the tensor cores' reads
         __syncwarp();
-        if (lane == 0) arrive_at(full0 + stage * 8);
+        if (lane == 0) ptx::mbar_arrive(&mine[stage]);
         if (++stage == kStages) {
           stage = 0;
           ph ^= 1u;
@@ -378,7 +453,7 @@ grouped_f32_kernel(const __grid_constant__ Args args) {
         }
         ptx::tc_fence_before();
         __syncwarp();
-        if (lane == 0) arrive_at(tempty0 + acc * 8);
+        if (lane == 0) arrive_relaxed_at(tempty0 + acc * 8);
         if (++acc == kAccs) {
           acc = 0;
           aph ^= 1u;
@@ -451,13 +526,18 @@ cudaError_t launch_grouped_f32(const GroupedShape& s, const GroupedPlan& p, Grou
   // 16-byte loads when every row of both operands starts on a 16-byte boundary
   auto aligned = [](const void* q) { return (reinterpret_cast<uintptr_t>(q) & 15) == 0; };
   const bool wide = aligned(a) && aligned(b) && s.K % 4 == 0 && s.O % 4 == 0;
+  auto even = [](const void* q, int64_t row) {
+    return (reinterpret_cast<uintptr_t>(q) & 7) == 0 && row % 2 == 0;
+  };
+  g.even_a = even(g.a, s.K);
+  g.even_b = even(g.b, which == kGroupedFwd ? s.K : s.O);
   auto* kernel = which == kGroupedFwd  ? (wide ? grouped_f32_kernel<kGroupedFwd, true>
                                                : grouped_f32_kernel<kGroupedFwd, false>)
                  : which == kGroupedDx ? (wide ? grouped_f32_kernel<kGroupedDx, true>
                                                : grouped_f32_kernel<kGroupedDx, false>)
                                        : (wide ? grouped_f32_kernel<kGroupedDw, true>
                                                : grouped_f32_kernel<kGroupedDw, false>);
-  const size_t smem = 1024 + kStages * kStageBytes + (2 * kStages + 2 * kAccs + 1 + 2 * kTileRing) * 8 +
+  const size_t smem = 1024 + kStages * kStageBytes + (3 * kStages + 2 * kAccs + 1 + 2 * kTileRing) * 8 +
                       kTileRing * sizeof(Tile) + 64;
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              static_cast<int>(smem));

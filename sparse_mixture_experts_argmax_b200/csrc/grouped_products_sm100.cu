@@ -394,7 +394,7 @@ grouped_sm100_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
       ptx::tc_fence_before();
       __syncwarp();
       if (lane == 0) {
-        if (ts.kb > 0) arrive_at(acc == 0 ? tempty0 : tempty1);
+        if (ts.kb > 0) arrive_relaxed_at(acc == 0 ? tempty0 : tempty1);
         ptx::mbar_arrive(&ring_empty[slot]);
       }
       if (ts.kb > 0 && ++acc == kAccs) {

@@ -93,6 +93,15 @@ __device__ __forceinline__ uint32_t leader_addr(const void* p) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(ptx::smem_u32(p)));
   return a;
 }
+// Arrivals on the other CTA's barrier.  A release at cluster scope waits for everything
+// its thread has in flight (dW of 16384 x 1024 x 4096 over 128 groups: 340 against
+// 266 us), so it is left to threads that have little: arrive_at publishes what this
+// CTA's threads wrote (and told the calling thread of); arrive_relaxed_at only says
+// that TMEM has been read (tcgen05.wait and the tcgen05 fences order that).
+__device__ __forceinline__ void arrive_relaxed_at(uint32_t cluster_bar) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar)
+               : "memory");
+}
 __device__ __forceinline__ void arrive_at(uint32_t cluster_bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar)
                : "memory");
