@@ -3,8 +3,8 @@
 //
 // An fp32 number is the sum of three bf16 numbers exactly: x rounded to 8 significant
 // bits, the rest rounded to 8, and the rest of that, which fits 8 (x = hi + mid + lo;
-// |mid| <= 2^-8 |x|, |lo| <= 2^-16 |x|; the pieces of a number that is not finite are the
-// number and zeros).  A product is then six bf16 products, each exact in fp32,
+// |mid| <= 2^-8 |x|, |lo| <= 2^-16 |x|; of a number that is not finite hi is not finite
+// either, and infinity times the other factor's zero rests is NaN).  A product is then six bf16 products, each exact in fp32,
 //   lo hi' + hi lo' + mid mid' + mid hi' + hi mid' + hi hi',
 // the three left out being at most 2^-23 of it together.  Six tensor-core products cost
 // 0.1 of one fp32 FMA per term at these units' rates (1.64 PFLOP/s against 75 TFLOP/s).
@@ -20,7 +20,7 @@
 // so that the 32 lanes of a store are consecutive in memory and no staging is needed.
 // Bound: the converting warps read fp32 operands from memory (any alignment, any width;
 // columns and rows past the end become zeros), split them and store three
-// 128-byte-swizzled tiles each, 24 instructions per 4 elements; at n = 128 the six
+// 128-byte-swizzled tiles each, 17 instructions per 2 elements; at n = 128 the six
 // products of a 64-deep step take 1536 cycles and its 12288 elements about 900 issue
 // cycles, for fewer rows the loads bound it.
 //
@@ -59,19 +59,23 @@ struct Args {
 };
 
 // The three pieces of two numbers, packed.  Rounding to 8 significant bits adds half a
-// unit to the magnitude and cuts; next to the largest number, where that would
-// overflow, hi is only cut.
+// unit to the magnitude and cuts (two integer instructions; the conversion instruction
+// made the kernel 1.5 times slower).  kCareful: hi is only cut next to the largest
+// number, where the rounding would overflow, and the rests of a number that is not finite
+// are zeros; otherwise `odd` becomes NaN where that is needed.
+template <bool kCareful>
 __device__ __forceinline__ void split2(float x0, float x1, uint32_t& hi, uint32_t& mid,
-                                       uint32_t& lo) {
+                                       uint32_t& lo, float& odd) {
   const float x[2] = {x0, x1};
   uint32_t p[2], q[2];
   float s[2];
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
     const float size = fabsf(x[j]);
-    p[j] = __float_as_uint(x[j]) + (size < 3e38f ? 0x8000u : 0u);
+    p[j] = __float_as_uint(x[j]) + (!kCareful || size < 3e38f ? 0x8000u : 0u);
     const float rest = x[j] - __uint_as_float(p[j] & 0xffff0000u);
-    const float r = size < __int_as_float(0x7f800000) ? rest : 0.f;
+    const float r = !kCareful || size < __int_as_float(0x7f800000) ? rest : 0.f;
+    if (!kCareful) odd = fmaf(r, 0.f, odd);
     q[j] = __float_as_uint(r) + 0x8000u;
     s[j] = r - __uint_as_float(q[j] & 0xffff0000u);
   }
@@ -377,9 +381,16 @@ grouped_f32_kernel(const __grid_constant__ Args args) {
           uint8_t* at = a + at0 + (q < R::kA ? q * R::kLines * 128
                                              : 3 * kAPlane + (q - R::kA) * R::kLines * 128);
           uint32_t w[3][R::kRun / 2];
+          const float* v = runs.v[s][j];
+          float odd = 0.f;
 #pragma unroll
           for (int i = 0; i < R::kRun / 2; ++i)
-            split2(runs.v[s][j][2 * i], runs.v[s][j][2 * i + 1], w[0][i], w[1][i], w[2][i]);
+            split2<!kWide>(v[2 * i], v[2 * i + 1], w[0][i], w[1][i], w[2][i], odd);
+          if (kWide && __builtin_expect(odd != 0.f, 0)) {     // (one test per run of 8 pays)
+#pragma unroll
+            for (int i = 0; i < R::kRun / 2; ++i)
+              split2<true>(v[2 * i], v[2 * i + 1], w[0][i], w[1][i], w[2][i], odd);
+          }
 #pragma unroll
           for (int i = 0; i < 3; ++i) {
             if constexpr (kWide)

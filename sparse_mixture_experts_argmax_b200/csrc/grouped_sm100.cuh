@@ -175,19 +175,23 @@ __device__ __forceinline__ uint64_t operand_desc(uint32_t base, int k) {
 }
 
 // Bounded wait for arrivals of the other CTA's threads (acquire at cluster scope).
+__device__ __forceinline__ bool cluster_bar_try(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(ptx::smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
 __device__ __forceinline__ bool cluster_bar_wait(uint64_t* bar, uint32_t parity,
                                                  volatile int* abort_flag, uint64_t limit_ns) {
+  if (cluster_bar_try(bar, parity)) return true;
   const uint64_t t0 = ptx::globaltimer_ns();
   for (uint32_t n = 1;; ++n) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(ptx::smem_u32(bar)), "r"(parity)
-        : "memory");
-    if (ok) return true;
+    if (cluster_bar_try(bar, parity)) return true;
     if ((n & 31u) == 0 && (*abort_flag || ptx::globaltimer_ns() - t0 > limit_ns)) return false;
   }
 }

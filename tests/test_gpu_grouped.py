@@ -266,3 +266,30 @@ def test_wrapper_refusals():
     square = torch.zeros((2, 16, 16), dtype=BF, device="cuda")
     with pytest.raises(swl.SwitchLayerError):
         swl.grouped_matmul(x, off, square, out=x)             # in place
+
+
+def test_f32_values_at_the_ends_of_the_range():
+    """The largest numbers (whose leading piece must not round to infinity), tiny ones,
+    infinities and NaN, by rows that start on 16-byte boundaries and by rows that do not."""
+    big = torch.finfo(F).max
+    for K in (64, 63):
+        x = torch.zeros((20, K), device="cuda")
+        W = torch.zeros((1, 8, K), device="cuda")
+        W[0, :, 3] = 1.0
+        W[0, 1, 3] = -0.5
+        x[:, 3] = torch.linspace(1, 2, 20, device="cuda")
+        x[4, 3], x[5, 3], x[6, 3] = big, float("inf"), float("nan")
+        x[7, 3], x[8, 3] = -big, 2.0 ** -100
+        off = torch.tensor([0, 20], dtype=torch.int32, device="cuda")
+        y = swl.grouped_matmul(x, off, W)
+        for r in range(20):
+            want = x[r, 3]
+            if r == 5:
+                # not finite, as documented.  By arithmetic it is NaN: W = 1 is the pieces
+                # 1, 0, 0, and among the six products infinity meets the zeros
+                assert not torch.isfinite(y[r]).any()
+            elif r == 6:
+                assert y[r].isnan().all()
+            else:
+                assert abs(float(y[r, 0]) - float(want)) <= 2.0 ** -22 * abs(float(want))
+                assert abs(float(y[r, 1]) + 0.5 * float(want)) <= 2.0 ** -22 * abs(float(want))
