@@ -508,8 +508,7 @@ norm_residual_bwd_kernel(const __grid_constant__ BwdArgsN a) {
 #pragma unroll
       for (int i = 0; i < E; ++i) {
         acc[0][i] = fmaf(g[i], v[i] * rho, acc[0][i]);
-        const float t = (kLayer ? b[i] - m0 : b[i]) - v[i] * m2;
-        D[i] = fmaf(t, rho, D[i]);
+        D[i] = fmaf(fmaf(-m2, v[i], kLayer ? b[i] - m0 : b[i]), rho, D[i]);
       }
     }
     store_row<T>(a.dx, row, valid, p.d, l, D);
@@ -520,40 +519,38 @@ norm_residual_bwd_kernel(const __grid_constant__ BwdArgsN a) {
     }
     if (!a.y) continue;
     const float gate = p.gate && valid ? p.gate[row] : 1.f;
-    // D becomes scale . D (no gate): the gate's gradient needs it without the gate
-    float sD[E];
+    // without the gate, which its own gradient needs; sc: the residual scale
+    float sc[E];
     if (p.scale) {
-      load_param(p.scale, p.d, l, w);
-#pragma unroll
-      for (int i = 0; i < E; ++i) sD[i] = D[i] * w[i];
+      load_param(p.scale, p.d, l, sc);
     } else {
 #pragma unroll
-      for (int i = 0; i < E; ++i) sD[i] = D[i];
+      for (int i = 0; i < E; ++i) sc[i] = 1.f;
     }
     if (p.w_post) {
       const float rho = center<kLayer>(y, p, l, buf, turn);
       load_param(p.w_post, p.d, l, w);
-      float bias[E];
+      float s[3] = {0.f, 0.f, 0.f};       // sums of scale D w, scale D w y^, scale D b
       if (kLayer && p.b_post) {
+        float bias[E];
         load_param(p.b_post, p.d, l, bias);
-      } else {
 #pragma unroll
-        for (int i = 0; i < E; ++i) bias[i] = 0.f;
+        for (int i = 0; i < E; ++i) {
+          acc[4][i] = fmaf(gate * D[i], bias[i], acc[4][i]);
+          s[2] = fmaf(D[i] * sc[i], bias[i], s[2]);
+        }
       }
-      float s[3] = {0.f, 0.f, 0.f};       // sD w, sD w y^, sD b
 #pragma unroll
       for (int i = 0; i < E; ++i) {
-        const float hat = y[i] * rho;
-        acc[4][i] = fmaf(gate * D[i], kLayer ? fmaf(hat, w[i], bias[i]) : hat * w[i], acc[4][i]);
-        acc[2][i] = fmaf(gate * sD[i], hat, acc[2][i]);
-        if constexpr (kLayer) {
-          acc[3][i] = fmaf(gate, sD[i], acc[3][i]);
-          s[2] = fmaf(sD[i], bias[i], s[2]);
-        }
-        sD[i] *= w[i];
-        if constexpr (kLayer) s[0] += sD[i];
-        s[1] = fmaf(sD[i], hat, s[1]);
-        y[i] = hat;
+        y[i] *= rho;                        // y^
+        const float gy = gate * y[i], z = D[i] * sc[i];
+        acc[2][i] = fmaf(z, gy, acc[2][i]);
+        if constexpr (kLayer) acc[3][i] = fmaf(gate, z, acc[3][i]);
+        D[i] *= w[i];
+        acc[4][i] = fmaf(D[i], gy, acc[4][i]);
+        D[i] *= sc[i];                      // scale D w
+        if constexpr (kLayer) s[0] += D[i];
+        s[1] = fmaf(D[i], y[i], s[1]);
       }
       if constexpr (kLayer) {
         row_sum(s, p.span, buf, turn);
@@ -565,21 +562,23 @@ norm_residual_bwd_kernel(const __grid_constant__ BwdArgsN a) {
       if (a.dgate && valid && l.tid == 0) a.dgate[row] = s[1] + s[2];
       const float m0 = s[0] * p.inv_d, m1 = s[1] * p.inv_d, f = gate * rho;
 #pragma unroll
-      for (int i = 0; i < E; ++i) sD[i] = ((kLayer ? sD[i] - m0 : sD[i]) - y[i] * m1) * f;
+      for (int i = 0; i < E; ++i) D[i] = fmaf(-m1, y[i], kLayer ? D[i] - m0 : D[i]) * f;
     } else {
       float s[1] = {0.f};
 #pragma unroll
       for (int i = 0; i < E; ++i) {
-        acc[4][i] = fmaf(gate * D[i], y[i], acc[4][i]);
-        s[0] = fmaf(sD[i], y[i], s[0]);
-        sD[i] *= gate;
+        const float gy = gate * y[i];
+        acc[4][i] = fmaf(D[i], gy, acc[4][i]);
+        D[i] *= sc[i];
+        s[0] = fmaf(D[i], y[i], s[0]);
+        D[i] *= gate;
       }
       if (a.dgate) {
         row_sum(s, p.span, buf, turn);
         if (valid && l.tid == 0) a.dgate[row] = s[0];
       }
     }
-    store_row<T>(a.dy, row, valid, p.d, l, sD);
+    store_row<T>(a.dy, row, valid, p.d, l, D);
   }
   if constexpr (R::kOn) asm volatile("cp.async.wait_all;" ::: "memory");
   __syncthreads();
@@ -660,8 +659,9 @@ Plan make_plan(int64_t T, int64_t d, int dtype, bool small_e, int sms,
   q.threads = 256;
   // E = 16 (bf16) once its threads fill the GPU's SMs with two warps per scheduler
   if (dtype == SWL_BF16 && d <= 4096) {
-    const bool wide = d > 2048 || (!small_e && q.V == 8 && d > 256 && T * (d / 16) >= sms * 256ll);
-    q.E = wide ? 16 : 8;
+    const bool few = small_e || q.V < 8;
+    q.E = few || (d <= 2048 && (d <= 256 || T * (d / 16) < sms * 256ll)) ? 8 : 16;
+    if (q.E == 8 && d > 2048) q.threads = 512;
   } else if (dtype == SWL_F32 && d <= 2048) {
     q.E = 8;
   } else {
@@ -681,10 +681,9 @@ bool dispatch(const Plan& q, int dtype, bool layer, F f) {
 #define SWL_V(T, V)                                      \
   if (q.threads == 256) {                                \
     if (q.E == 8) { SWL_L(T, V, 8, 256) }                \
-    if constexpr (sizeof(T) == 2) { SWL_L(T, V, 16, 256) } \
+    if constexpr (sizeof(T) * V == 16 && sizeof(T) == 2) { SWL_L(T, V, 16, 256) } \
   }                                                      \
-  if constexpr (sizeof(T) == 4)                          \
-    if (q.E == 8) { SWL_L(T, V, 8, 512) }                \
+  if (q.E == 8) { SWL_L(T, V, 8, 512) }                  \
   if (q.E == 16) { SWL_L(T, V, 16, 512) }                \
   SWL_L(T, V, 32, 512)
   if (dtype == SWL_BF16) {
