@@ -1,13 +1,15 @@
 // Products grouped by expert on the tensor cores for fp32 tensors: y = x W^T + b,
 // dx = dy W and dW = dy^T x over ragged row ranges.
 //
-// An fp32 number is the sum of three bf16 numbers exactly: x rounded to 8 significant
-// bits, the rest rounded to 8, and the rest of that, which fits 8 (x = hi + mid + lo;
-// |mid| <= 2^-8 |x|, |lo| <= 2^-16 |x|; of a number that is not finite hi is not finite
-// either, and infinity times the other factor's zero rests is NaN).  A product is then six bf16 products, each exact in fp32,
-//   lo hi' + hi lo' + mid mid' + mid hi' + hi mid' + hi hi',
-// the three left out being at most 2^-23 of it together.  Six tensor-core products cost
-// 0.1 of one fp32 FMA per term at these units' rates (1.64 PFLOP/s against 75 TFLOP/s).
+// An fp32 number is the sum of three bf16 numbers exactly: its leading 8 significant
+// bits, the next 8 and the last 8 (x = hi + mid + lo, cut, not rounded: two instructions
+// a piece, and nothing overflows; of a number that is not finite a rest is NaN).  A
+// product is then eight bf16 products, each exact in fp32,
+//   lo mid' + mid lo' + lo hi' + hi lo' + mid mid' + mid hi' + hi mid' + hi hi',
+// the ninth, lo lo', being under 2^-28 of it.  Eight tensor-core products cost 0.2 of
+// one fp32 FMA per term at these units' rates (1.64 PFLOP/s against 75 TFLOP/s).  Six
+// products of pieces rounded to nearest leave out 2^-23, and the rounding cost more than
+// the two products.
 //
 // The tensor cores cut their running sums instead of rounding them, so a long sum
 // would drift by half a unit per step.  Sums in TMEM therefore run over 64 terms only,
@@ -20,9 +22,9 @@
 // so that the 32 lanes of a store are consecutive in memory and no staging is needed.
 // Bound: the converting warps read fp32 operands from memory (any alignment, any width;
 // columns and rows past the end become zeros), split them and store three
-// 128-byte-swizzled tiles each, 17 instructions per 2 elements; at n = 128 the six
-// products of a 64-deep step take 1536 cycles and its 12288 elements about 900 issue
-// cycles, for fewer rows the loads bound it.
+// 128-byte-swizzled tiles each, 11 instructions per 2 elements; at n = 128 the eight
+// products of a 64-deep step take 2048 cycles and its 12288 elements about 600 issue
+// cycles of splitting, for fewer rows the loads bound it.
 //
 // Roles of a CTA's 20 warps: 0 MMA issuer (first CTA only), 1 TMEM, 2 tile decoder, 3
 // relay between the converters and the first CTA, 4-11 sums and stores (two warps per lane quarter), 12-19 converters.
@@ -58,30 +60,16 @@ struct Args {
   bool even_a, even_b;   // every row of the operand starts on an 8-byte boundary
 };
 
-// The three pieces of two numbers, packed.  Rounding to 8 significant bits adds half a
-// unit to the magnitude and cuts (two integer instructions; the conversion instruction
-// made the kernel 1.5 times slower).  kCareful: hi is only cut next to the largest
-// number, where the rounding would overflow, and the rests of a number that is not finite
-// are zeros; otherwise `odd` becomes NaN where that is needed.
-template <bool kCareful>
+// The three pieces of two numbers, packed.
 __device__ __forceinline__ void split2(float x0, float x1, uint32_t& hi, uint32_t& mid,
-                                       uint32_t& lo, float& odd) {
-  const float x[2] = {x0, x1};
-  uint32_t p[2], q[2];
-  float s[2];
-#pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    const float size = fabsf(x[j]);
-    p[j] = __float_as_uint(x[j]) + (!kCareful || size < 3e38f ? 0x8000u : 0u);
-    const float rest = x[j] - __uint_as_float(p[j] & 0xffff0000u);
-    const float r = !kCareful || size < __int_as_float(0x7f800000) ? rest : 0.f;
-    if (!kCareful) odd = fmaf(r, 0.f, odd);
-    q[j] = __float_as_uint(r) + 0x8000u;
-    s[j] = r - __uint_as_float(q[j] & 0xffff0000u);
-  }
-  hi = __byte_perm(p[0], p[1], 0x7632);
-  mid = __byte_perm(q[0], q[1], 0x7632);
-  lo = __byte_perm(__float_as_uint(s[0]), __float_as_uint(s[1]), 0x7632);
+                                       uint32_t& lo) {
+  const float r0 = x0 - __uint_as_float(__float_as_uint(x0) & 0xffff0000u);
+  const float r1 = x1 - __uint_as_float(__float_as_uint(x1) & 0xffff0000u);
+  const float s0 = r0 - __uint_as_float(__float_as_uint(r0) & 0xffff0000u);
+  const float s1 = r1 - __uint_as_float(__float_as_uint(r1) & 0xffff0000u);
+  hi = __byte_perm(__float_as_uint(x0), __float_as_uint(x1), 0x7632);
+  mid = __byte_perm(__float_as_uint(r0), __float_as_uint(r1), 0x7632);
+  lo = __byte_perm(__float_as_uint(s0), __float_as_uint(s1), 0x7632);
 }
 
 // What a converting thread holds of a stage: kCount runs of kRun consecutive floats of
@@ -268,9 +256,9 @@ grouped_f32_kernel(const __grid_constant__ Args args) {
           const uint32_t a = ptx::smem_u32(smem + stage * kStageBytes), b = a + 3 * kAPlane;
           const uint32_t d = tmem + static_cast<uint32_t>(acc * kAccCols);
           // pieces 0 hi, 1 mid, 2 lo; the small products first
-          constexpr int kPa[6] = {2, 0, 1, 1, 0, 0}, kPb[6] = {0, 2, 1, 0, 1, 0};
+          constexpr int kPa[8] = {2, 1, 2, 0, 1, 1, 0, 0}, kPb[8] = {1, 2, 0, 2, 1, 0, 1, 0};
 #pragma unroll
-          for (int p = 0; p < 6; ++p)
+          for (int p = 0; p < 8; ++p)
 #pragma unroll
             for (int k = 0; k < kBK / 16; ++k)
               pair_mma(d, operand_desc<kAmn>(a + kPa[p] * kAPlane, k),
@@ -382,15 +370,9 @@ grouped_f32_kernel(const __grid_constant__ Args args) {
                                              : 3 * kAPlane + (q - R::kA) * R::kLines * 128);
           uint32_t w[3][R::kRun / 2];
           const float* v = runs.v[s][j];
-          float odd = 0.f;
 #pragma unroll
           for (int i = 0; i < R::kRun / 2; ++i)
-            split2<!kWide>(v[2 * i], v[2 * i + 1], w[0][i], w[1][i], w[2][i], odd);
-          if (kWide && __builtin_expect(odd != 0.f, 0)) {     // (one test per run of 8 pays)
-#pragma unroll
-            for (int i = 0; i < R::kRun / 2; ++i)
-              split2<true>(v[2 * i], v[2 * i + 1], w[0][i], w[1][i], w[2][i], odd);
-          }
+            split2(v[2 * i], v[2 * i + 1], w[0][i], w[1][i], w[2][i]);
 #pragma unroll
           for (int i = 0; i < 3; ++i) {
             if constexpr (kWide)

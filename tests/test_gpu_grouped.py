@@ -3,8 +3,7 @@
 Tolerance: a sum of n products of exact factors in fp32, every partial sum off by at
 most 2^-23 of the sum S of the absolute products (rounded or truncated), is off by at
 most (n + 2) 2^-23 S; then half a step of the output type.  The products that stand
-for one of two fp32 numbers leave out at most 2^-23 of it, another 2^-23 S (and the
-squares of these, well under a fourth).
+for one of two fp32 numbers leave out under 2^-28 of it.
 """
 from __future__ import annotations
 
@@ -286,7 +285,7 @@ def test_f32_values_at_the_ends_of_the_range():
             want = x[r, 3]
             if r == 5:
                 # not finite, as documented.  By arithmetic it is NaN: W = 1 is the pieces
-                # 1, 0, 0, and among the six products infinity meets the zeros
+                # 1, 0, 0, and among the products infinity meets the zeros
                 assert not torch.isfinite(y[r]).any()
             elif r == 6:
                 assert y[r].isnan().all()
