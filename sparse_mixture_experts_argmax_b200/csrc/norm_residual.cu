@@ -101,6 +101,36 @@ struct Vec<__nv_bfloat16, 1> {
   }
 };
 
+// Two fp32 operations in one instruction, each rounded as by itself: the element-wise
+// work is what these kernels issue most.  d may be an operand.
+__device__ __forceinline__ void fma2(float* d, const float* a, const float* b, const float* c) {
+  asm("{\n\t.reg .b64 x, y, z;\n\t"
+      "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+      "fma.rn.f32x2 z, x, y, z;\n\tmov.b64 {%0, %1}, z;\n\t}"
+      : "=f"(d[0]), "=f"(d[1])
+      : "f"(a[0]), "f"(a[1]), "f"(b[0]), "f"(b[1]), "f"(c[0]), "f"(c[1]));
+}
+__device__ __forceinline__ void mul2(float* d, const float* a, const float* b) {
+  asm("{\n\t.reg .b64 x, y;\n\t"
+      "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "mul.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "=f"(d[0]), "=f"(d[1])
+      : "f"(a[0]), "f"(a[1]), "f"(b[0]), "f"(b[1]));
+}
+__device__ __forceinline__ void add2(float* d, const float* a, const float* b) {
+  asm("{\n\t.reg .b64 x, y;\n\t"
+      "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "add.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "=f"(d[0]), "=f"(d[1])
+      : "f"(a[0]), "f"(a[1]), "f"(b[0]), "f"(b[1]));
+}
+// A scalar for both halves.
+struct Both {
+  float v[2];
+  __device__ __forceinline__ explicit Both(float x) : v{x, x} {}
+  __device__ __forceinline__ operator const float*() const { return v; }
+};
+
 struct Params {
   const float* w_pre;
   const float* b_pre;
@@ -297,22 +327,29 @@ __device__ __forceinline__ void row_sum(float (&v)[N], int span, float (*buf)[4]
   }
 }
 
+// v becomes v - mu in the row's columns, zero behind them.
+template <int V, int E>
+__device__ __forceinline__ void subtract(float (&v)[E], float mu, int d, const Lane<V, E>& l) {
+#pragma unroll
+  for (int i = 0; i < E; ++i) v[i] = l.col(i / V) < d ? v[i] - mu : 0.f;
+}
+
 // v becomes v - mu (layer norm; v itself for RMS norm); returns rho.
 template <bool kLayer, int V, int E>
 __device__ __forceinline__ float center(float (&v)[E], const Params& p, const Lane<V, E>& l,
                                         float (*buf)[4][kMaxWarps], int& turn) {
   if constexpr (kLayer) {
-    float s[1] = {0.f};
+    float t[2] = {0.f, 0.f};
 #pragma unroll
-    for (int i = 0; i < E; ++i) s[0] += v[i];       // columns past d hold zeros
+    for (int i = 0; i < E; i += 2) add2(t, t, v + i);       // columns past d hold zeros
+    float s[1] = {t[0] + t[1]};
     row_sum(s, p.span, buf, turn);
-    const float mu = s[0] * p.inv_d;
-#pragma unroll
-    for (int i = 0; i < E; ++i) v[i] = l.col(i / V) < p.d ? v[i] - mu : 0.f;
+    subtract(v, s[0] * p.inv_d, p.d, l);
   }
-  float s[1] = {0.f};
+  float t[2] = {0.f, 0.f};
 #pragma unroll
-  for (int i = 0; i < E; ++i) s[0] = fmaf(v[i], v[i], s[0]);
+  for (int i = 0; i < E; i += 2) fma2(t, v + i, v + i, t);
+  float s[1] = {t[0] + t[1]};
   row_sum(s, p.span, buf, turn);
   return rsqrtf(fmaf(s[0], p.inv_d, p.eps));
 }
@@ -369,33 +406,44 @@ norm_residual_kernel(const __grid_constant__ FwdArgs a) {
         if (kLayer && p.b_post) {
           float b[E];
           load_param(p.b_post, p.d, l, b);
+          const Both rr(rho);
 #pragma unroll
-          for (int i = 0; i < E; ++i) u[i] = fmaf(u[i] * rho, w[i], b[i]);
+          for (int i = 0; i < E; i += 2) {
+            mul2(u + i, u + i, rr);
+            fma2(u + i, u + i, w + i, b + i);
+          }
         } else {
           f *= rho;
 #pragma unroll
-          for (int i = 0; i < E; ++i) u[i] *= w[i];
+          for (int i = 0; i < E; i += 2) mul2(u + i, u + i, w + i);
         }
       }
       if (p.scale) {
         load_param(p.scale, p.d, l, w);
 #pragma unroll
-        for (int i = 0; i < E; ++i) u[i] *= w[i];
+        for (int i = 0; i < E; i += 2) mul2(u + i, u + i, w + i);
       }
+      const Both ff(f);
 #pragma unroll
-      for (int i = 0; i < E; ++i) r[i] = fmaf(f, u[i], r[i]);
+      for (int i = 0; i < E; i += 2) fma2(r + i, ff, u + i, r + i);
       store_row<T>(a.r, row, valid, p.d, l, r);
     }
     if (a.h) {
-      const float rho = center<kLayer>(r, p, l, buf, turn);
+      const Both rr(center<kLayer>(r, p, l, buf, turn));
       load_param(p.w_pre, p.d, l, w);
       if (kLayer && p.b_pre) {
         load_param(p.b_pre, p.d, l, u);
 #pragma unroll
-        for (int i = 0; i < E; ++i) r[i] = fmaf(r[i] * rho, w[i], u[i]);
+        for (int i = 0; i < E; i += 2) {
+          mul2(r + i, r + i, rr);
+          fma2(r + i, r + i, w + i, u + i);
+        }
       } else {
 #pragma unroll
-        for (int i = 0; i < E; ++i) r[i] = r[i] * rho * w[i];
+        for (int i = 0; i < E; i += 2) {
+          mul2(r + i, r + i, rr);
+          mul2(r + i, r + i, w + i);
+        }
       }
       store_row<T>(a.h, row, valid, p.d, l, r);
     }
@@ -411,24 +459,24 @@ __device__ __forceinline__ float center_with(float (&v)[E], const float (&a)[E],
                                              int& turn, float& m0, float& m1) {
   m0 = 0.f;
   if constexpr (kLayer) {
-    float s[2] = {0.f, 0.f};
+    float t[2] = {0.f, 0.f}, u[2] = {0.f, 0.f};
 #pragma unroll
-    for (int i = 0; i < E; ++i) {
-      s[0] += v[i];
-      s[1] += a[i];
+    for (int i = 0; i < E; i += 2) {
+      add2(t, t, v + i);
+      add2(u, u, a + i);
     }
+    float s[2] = {t[0] + t[1], u[0] + u[1]};
     row_sum(s, p.span, buf, turn);
-    const float mu = s[0] * p.inv_d;
     m0 = s[1] * p.inv_d;
-#pragma unroll
-    for (int i = 0; i < E; ++i) v[i] = l.col(i / V) < p.d ? v[i] - mu : 0.f;
+    subtract(v, s[0] * p.inv_d, p.d, l);
   }
-  float s[2] = {0.f, 0.f};
+  float t[2] = {0.f, 0.f}, u[2] = {0.f, 0.f};
 #pragma unroll
-  for (int i = 0; i < E; ++i) {
-    s[0] = fmaf(v[i], v[i], s[0]);
-    s[1] = fmaf(a[i], v[i], s[1]);
+  for (int i = 0; i < E; i += 2) {
+    fma2(t, v + i, v + i, t);
+    fma2(u, a + i, v + i, u);
   }
+  float s[2] = {t[0] + t[1], u[0] + u[1]};
   row_sum(s, p.span, buf, turn);
   m1 = s[1] * p.inv_d;
   return rsqrtf(fmaf(s[0], p.inv_d, p.eps));
@@ -495,20 +543,22 @@ norm_residual_bwd_kernel(const __grid_constant__ BwdArgsN a) {
     }
     if (a.dh) {
       load_param(p.w_pre, p.d, l, w);
-      if constexpr (kLayer) {
 #pragma unroll
-        for (int i = 0; i < E; ++i) acc[1][i] += g[i];
+      for (int i = 0; i < E; i += 2) {
+        if constexpr (kLayer) add2(acc[1] + i, acc[1] + i, g + i);
+        mul2(w + i, g + i, w + i);          // a = w dh
       }
-      float b[E];
-#pragma unroll
-      for (int i = 0; i < E; ++i) b[i] = g[i] * w[i];
       float m0, m1;
-      const float rho = center_with<kLayer>(v, b, p, l, buf, turn, m0, m1);
-      const float m2 = m1 * rho * rho;
+      const float rho = center_with<kLayer>(v, w, p, l, buf, turn, m0, m1);
+      const Both rr(rho), mm0(-m0), mm2(-m1 * rho * rho);
 #pragma unroll
-      for (int i = 0; i < E; ++i) {
-        acc[0][i] = fmaf(g[i], v[i] * rho, acc[0][i]);
-        D[i] = fmaf(fmaf(-m2, v[i], kLayer ? b[i] - m0 : b[i]), rho, D[i]);
+      for (int i = 0; i < E; i += 2) {
+        float t[2];
+        if constexpr (kLayer) add2(w + i, w + i, mm0);
+        fma2(t, mm2, v + i, w + i);
+        fma2(D + i, t, rr, D + i);
+        mul2(v + i, v + i, rr);
+        fma2(acc[0] + i, g + i, v + i, acc[0] + i);
       }
     }
     store_row<T>(a.dx, row, valid, p.d, l, D);
@@ -531,27 +581,37 @@ norm_residual_bwd_kernel(const __grid_constant__ BwdArgsN a) {
       const float rho = center<kLayer>(y, p, l, buf, turn);
       load_param(p.w_post, p.d, l, w);
       float s[3] = {0.f, 0.f, 0.f};       // sums of scale D w, scale D w y^, scale D b
+      const Both gg(gate), rr(rho);
+      float t0[2] = {0.f, 0.f}, t1[2] = {0.f, 0.f};
       if (kLayer && p.b_post) {
-        float bias[E];
+        float bias[E], t2[2] = {0.f, 0.f};
         load_param(p.b_post, p.d, l, bias);
 #pragma unroll
-        for (int i = 0; i < E; ++i) {
-          acc[4][i] = fmaf(gate * D[i], bias[i], acc[4][i]);
-          s[2] = fmaf(D[i] * sc[i], bias[i], s[2]);
+        for (int i = 0; i < E; i += 2) {
+          float z[2];
+          mul2(z, gg, D + i);
+          fma2(acc[4] + i, z, bias + i, acc[4] + i);
+          mul2(z, D + i, sc + i);
+          fma2(t2, z, bias + i, t2);
         }
+        s[2] = t2[0] + t2[1];
       }
 #pragma unroll
-      for (int i = 0; i < E; ++i) {
-        y[i] *= rho;                        // y^
-        const float gy = gate * y[i], z = D[i] * sc[i];
-        acc[2][i] = fmaf(z, gy, acc[2][i]);
-        if constexpr (kLayer) acc[3][i] = fmaf(gate, z, acc[3][i]);
-        D[i] *= w[i];
-        acc[4][i] = fmaf(D[i], gy, acc[4][i]);
-        D[i] *= sc[i];                      // scale D w
-        if constexpr (kLayer) s[0] += D[i];
-        s[1] = fmaf(D[i], y[i], s[1]);
+      for (int i = 0; i < E; i += 2) {
+        float gy[2], z[2];
+        mul2(y + i, y + i, rr);             // y^
+        mul2(gy, gg, y + i);
+        mul2(z, D + i, sc + i);
+        fma2(acc[2] + i, z, gy, acc[2] + i);
+        if constexpr (kLayer) fma2(acc[3] + i, gg, z, acc[3] + i);
+        mul2(D + i, D + i, w + i);
+        fma2(acc[4] + i, D + i, gy, acc[4] + i);
+        mul2(D + i, z, w + i);              // scale D w
+        if constexpr (kLayer) add2(t0, t0, D + i);
+        fma2(t1, D + i, y + i, t1);
       }
+      s[0] = t0[0] + t0[1];
+      s[1] = t1[0] + t1[1];
       if constexpr (kLayer) {
         row_sum(s, p.span, buf, turn);
       } else {
@@ -560,20 +620,27 @@ norm_residual_bwd_kernel(const __grid_constant__ BwdArgsN a) {
         s[1] = one[0];
       }
       if (a.dgate && valid && l.tid == 0) a.dgate[row] = s[1] + s[2];
-      const float m0 = s[0] * p.inv_d, m1 = s[1] * p.inv_d, f = gate * rho;
+      const Both m0(-s[0] * p.inv_d), m1(-s[1] * p.inv_d), f(gate * rho);
 #pragma unroll
-      for (int i = 0; i < E; ++i) D[i] = fmaf(-m1, y[i], kLayer ? D[i] - m0 : D[i]) * f;
+      for (int i = 0; i < E; i += 2) {
+        if constexpr (kLayer) add2(D + i, D + i, m0);
+        fma2(D + i, m1, y + i, D + i);
+        mul2(D + i, D + i, f);
+      }
     } else {
-      float s[1] = {0.f};
+      const Both gg(gate);
+      float t1[2] = {0.f, 0.f};
 #pragma unroll
-      for (int i = 0; i < E; ++i) {
-        const float gy = gate * y[i];
-        acc[4][i] = fmaf(D[i], gy, acc[4][i]);
-        D[i] *= sc[i];
-        s[0] = fmaf(D[i], y[i], s[0]);
-        D[i] *= gate;
+      for (int i = 0; i < E; i += 2) {
+        float gy[2];
+        mul2(gy, gg, y + i);
+        fma2(acc[4] + i, D + i, gy, acc[4] + i);
+        mul2(D + i, D + i, sc + i);
+        fma2(t1, D + i, y + i, t1);
+        mul2(D + i, D + i, gg);
       }
       if (a.dgate) {
+        float s[1] = {t1[0] + t1[1]};
         row_sum(s, p.span, buf, turn);
         if (valid && l.tid == 0) a.dgate[row] = s[0];
       }
