@@ -370,7 +370,7 @@ adamw_kernel(const __grid_constant__ AdamwTable<kMax> a) {
   __shared__ float s_rate, s_root2;
   __shared__ double s_lr;
   __shared__ unsigned s_key;
-  const int t = max(a.step[0], 0) + 1;
+  const int t = min(max(a.step[0], 0), INT_MAX - 1) + 1;
   if (threadIdx.x == 0) {
     const double lr = a.lr * (a.lr_scale ? static_cast<double>(*a.lr_scale) : 1.0);
     s_lr = lr;

@@ -184,9 +184,9 @@ grouped_sm100_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
         if constexpr (W == kGroupedDw) {
           // written by another kernel's ordinary stores
           map = args.maps + 2 * ts.e + (is_a ? 0 : 1);
-          if (ts.e != last_e)
+          if (ts.e != last_e && ts.kb > 0)
             asm volatile("fence.proxy.tensormap::generic.acquire.gpu [%0], 128;" ::"l"(map) : "memory");
-          last_e = ts.e;
+          if (ts.kb > 0) last_e = ts.e;
         }
         const int half = ts.n >> 1;              // this CTA's rows of B
         const int m0 = ts.m0 + static_cast<int>(rank) * 128;
