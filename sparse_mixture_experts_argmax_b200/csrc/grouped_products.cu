@@ -361,7 +361,7 @@ extern "C" swl_status switch_layer_grouped_matmul(int64_t R, int64_t K, int64_t 
   const int sms = grouped_sms();
   if (sms <= 0) return SWL_ERR_CUDA;
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
-  if (R > 0 && R <= kFewRows)
+  if (grouped_few(s))
     return launch_grouped_few(s, p, offsets, x, W, bias, y, cs) == cudaSuccess ? SWL_OK
                                                                               : SWL_ERR_CUDA;
   if (launch_grouped_plan(s, p, offsets, tile_rows(s), nullptr, cs) != cudaSuccess)

@@ -25,6 +25,11 @@
 // Tiles go round the pairs in order; the row tiles of a group are consecutive.
 // Every wait is bounded: one that runs out sets the device error word and the CTA
 // drains and leaves.
+//
+// Bound: tensor cores for groups of many rows (32768 x 2048 by 8 groups of 5120 x 2048:
+// 490 us, 1.40 PFLOP/s, 0.86 of the burst peak), W's bytes for few (16384 rows over 128
+// groups, 1024 -> 4096: y 207 us and dx 193 us where the bytes take 189 us), dW's stores
+// (the same sizes: 258 us; a plain fill of 1.07 GB takes 275 us).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -422,9 +427,11 @@ bool grouped_sm100_templates(const GroupedShape& s, const void* dy, const void* 
   return encode_tmap_bf16(&out[0], dy, 2, dd, box) && encode_tmap_bf16(&out[1], x, 2, dx, box);
 }
 
-// Rows of B per tile, at most: 256 once the groups have 48 rows on average (one pass
-// over W for most), 64 for fewer rows (more stages of W fit).
-int grouped_sm100_tile_rows(const GroupedShape& s) { return s.R >= 48 * s.N ? 256 : 64; }
+// Rows of B per tile, at most: 256 from 40 rows per group on average on (one pass over W
+// for most groups), 64 below (more stages of W fit).  128 groups of 2048 x 1024, rows
+// spread unevenly: 24 per group 95 us with 256 and 90 with 64, 40: 99 and 99, 64: 104
+// and 117, 96: 110 and 166.
+int grouped_sm100_tile_rows(const GroupedShape& s) { return s.R >= 40 * s.N ? 256 : 64; }
 
 cudaError_t launch_grouped_sm100(const GroupedShape& s, const GroupedPlan& p, GroupedWhich which,
                                  const int* offsets, const void* a, const void* b,

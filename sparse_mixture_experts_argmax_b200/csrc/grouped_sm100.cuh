@@ -94,8 +94,8 @@ __device__ __forceinline__ uint32_t leader_addr(const void* p) {
   return a;
 }
 // Arrivals on the other CTA's barrier.  A release at cluster scope waits for everything
-// its thread has in flight (dW of 16384 x 1024 x 4096 over 128 groups: 340 against
-// 266 us), so it is left to threads that have little: arrive_at publishes what this
+// its thread has in flight (dW of 16384 x 1024 x 4096 over 128 groups: 334 against
+// 259 us), so it is left to threads that have little: arrive_at publishes what this
 // CTA's threads wrote (and told the calling thread of); arrive_relaxed_at only says
 // that TMEM has been read (tcgen05.wait and the tcgen05 fences order that).
 __device__ __forceinline__ void arrive_relaxed_at(uint32_t cluster_bar) {
