@@ -31,7 +31,8 @@
 // read in whole vectors (fp32 16 bytes, bf16 8, codes 4) and a block's two maxima
 // are five shuffles each.  The tensor table travels in the kernel's parameters
 // (nothing to copy or allocate, so a captured call replays as it is) and the grid is
-// persistent, so the corrections are computed once per CTA.
+// persistent, so the corrections are computed once per CTA (256 threads, three CTAs per
+// SM: 635 us at the size below; two 637, 128 threads with five or six CTAs 657 and 653).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

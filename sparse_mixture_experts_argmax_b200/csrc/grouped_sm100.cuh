@@ -55,7 +55,8 @@ __device__ __forceinline__ Tile decode_tile(int t, int total, const TileShape& s
     }
     const int p0 = __ldg(s.prefix + lo), nts = __ldg(s.prefix + lo + 1) - p0;
     // bands of kBand row tiles go through all of W, row tiles fastest: the tiles
-    // running together share few rows of x and few of W
+    // running together share few rows of x and few of W (one group of 32768 x 2048 by
+    // 5120 x 2048: 573 us with all its row tiles in one band, 483 with bands of 8)
     const int local = t - p0 * s.m_tiles;
     const int band = local / (kBand * s.m_tiles);
     const int r = local - band * kBand * s.m_tiles;
