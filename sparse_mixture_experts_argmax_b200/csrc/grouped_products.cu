@@ -60,13 +60,16 @@ struct MapPair {
 // CTA 0 counts (a group has at most R / tile_rows + 1 tiles, so the counts fit an int);
 // the others make dW's maps, a warp per group: the templates with the rows ended at
 // the group's last one.  A map's end is clipped to R whatever the offsets say.
+// The trigger follows the wait: what runs behind the plan starts when the call's inputs
+// are complete, so only the plan's own outputs change under it (these it reads by
+// ordinary loads), and its other operands may go through the read-only path.
 __global__ void __launch_bounds__(kPlanThreads)
 grouped_plan_kernel(const __grid_constant__ PlanArgs a, const __grid_constant__ MapPair templates) {
   __shared__ int warp_sums[32];
-  pdl_trigger();
   pdl_wait();
-  const int* __restrict__ off = a.off;
-  int* __restrict__ prefix = a.prefix;
+  pdl_trigger();
+  const int* off = a.off;
+  int* prefix = a.prefix;
   WsHeader* hdr = a.hdr;
   const int N = a.N, R = a.R, tile_rows = a.tile_rows;
   if (blockIdx.x > 0) {
@@ -113,7 +116,7 @@ grouped_plan_kernel(const __grid_constant__ PlanArgs a, const __grid_constant__ 
 }
 
 // Last e with P[e] <= q (P[N] > q).
-__device__ __forceinline__ int find_group(const int* __restrict__ P, int N, int q) {
+__device__ __forceinline__ int find_group(const int* P, int N, int q) {
   int lo = 0, hi = N;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
@@ -128,7 +131,8 @@ __device__ __forceinline__ int find_group(const int* __restrict__ P, int N, int 
 // interleaved runs of rows (a warp each, 16-byte loads for bf16), then the runs in order.
 // A group of one tile is then done; the tiles of a larger one leave fp32 partial sums
 // that the second kernel adds in order, so a group of many rows is spread over as many
-// CTAs as it has tiles.  Bound: one read of dy.
+// CTAs as it has tiles.  Bound: one read of dy.  (prefix and part are written by the
+// kernels just before: ordinary loads.)
 template <typename T>
 struct BiasVec;
 template <>
@@ -152,10 +156,8 @@ struct BiasVec<float> {
 
 template <typename T>
 __global__ void __launch_bounds__(256)
-grouped_bias_tile_kernel(const T* __restrict__ dy, const int* __restrict__ off,
-                         const int* __restrict__ prefix, T* __restrict__ db,
-                         float* __restrict__ part, const WsHeader* hdr, int O, int N,
-                         int tile_rows) {
+grouped_bias_tile_kernel(const T* __restrict__ dy, const int* off, const int* prefix, T* db,
+                         float* part, const WsHeader* hdr, int O, int N, int tile_rows) {
   constexpr int V = BiasVec<T>::V;
   __shared__ float buf[8][32 * V];
   pdl_trigger();
@@ -190,8 +192,8 @@ grouped_bias_tile_kernel(const T* __restrict__ dy, const int* __restrict__ off,
 
 template <typename T>
 __global__ void __launch_bounds__(256)
-grouped_bias_sum_kernel(const int* __restrict__ prefix, T* __restrict__ db,
-                        const float* __restrict__ part, const WsHeader* hdr, int O, int N) {
+grouped_bias_sum_kernel(const int* prefix, T* db, const float* part, const WsHeader* hdr, int O,
+                        int N) {
   pdl_trigger();
   pdl_wait();
   if (hdr->err) return;

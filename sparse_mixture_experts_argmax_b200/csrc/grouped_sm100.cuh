@@ -13,7 +13,9 @@ struct Tile {
   int e, m0, row0, rows, n, n0, kb;
 };
 
-// What the tile decoder needs.
+// What the tile decoder needs.  off and prefix are read by ordinary loads: the plan writes
+// prefix while the product's CTAs may be on the GPU already, which rules out the read-only
+// path (its lines may be older than the plan's wait).
 struct TileShape {
   const int* off;
   const int* prefix;
@@ -41,8 +43,8 @@ __device__ __forceinline__ Tile decode_tile(int t, int total, const TileShape& s
     const int r = t - ts.e * per;
     ts.m0 = r / s.n_tiles * 256;
     ts.n0 = (r % s.n_tiles) * s.bn_cols;
-    ts.row0 = __ldg(s.off + ts.e);
-    ts.rows = __ldg(s.off + ts.e + 1) - ts.row0;
+    ts.row0 = s.off[ts.e];
+    ts.rows = s.off[ts.e + 1] - ts.row0;
     ts.n = min(s.bn_cols, (s.cols - ts.n0 + 127) & ~127);
     ts.kb = (ts.rows + kBK - 1) / kBK;
   } else {
@@ -50,10 +52,10 @@ __device__ __forceinline__ Tile decode_tile(int t, int total, const TileShape& s
     int lo = 0, hi = s.N;
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if (__ldg(s.prefix + mid) <= q) lo = mid;
+      if (s.prefix[mid] <= q) lo = mid;
       else hi = mid;
     }
-    const int p0 = __ldg(s.prefix + lo), nts = __ldg(s.prefix + lo + 1) - p0;
+    const int p0 = s.prefix[lo], nts = s.prefix[lo + 1] - p0;
     // bands of kBand row tiles go through all of W, row tiles fastest: the tiles
     // running together share few rows of x and few of W (one group of 32768 x 2048 by
     // 5120 x 2048: 573 us with all its row tiles in one band, 483 with bands of 8)
@@ -66,7 +68,7 @@ __device__ __forceinline__ Tile decode_tile(int t, int total, const TileShape& s
     ts.m0 = r / in_band * 256;
     // the group's rows in nts parts of whole units, as even as they go: no short
     // tile that loads as much W as a full one
-    const int begin = __ldg(s.off + lo), rows = __ldg(s.off + lo + 1) - begin;
+    const int begin = s.off[lo], rows = s.off[lo + 1] - begin;
     const int units = (rows + kUnit - 1) / kUnit;
     const int per = units / nts, more = units - per * nts;
     const int first = (nt * per + min(nt, more)) * kUnit;

@@ -498,7 +498,7 @@ norm_residual_bwd_kernel(const __grid_constant__ BwdArgsN a) {
   const Lane<V, E> l(p.span);
   using R = Ring<T, V, E, 4>;
   R ring(smem);
-  pdl_trigger();
+  if (a.wanted) pdl_trigger();      // the column sums' kernel follows
   const int64_t stride = static_cast<int64_t>(gridDim.x) * l.groups;
   const int64_t first = static_cast<int64_t>(blockIdx.x) * l.groups;
   int turn = 0;
