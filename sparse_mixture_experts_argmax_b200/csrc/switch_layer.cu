@@ -124,39 +124,49 @@ static PFN_encodeTiled get_encode_tiled() {
   return fn;
 }
 
+// Row-major bf16 tensor of `rank` dimensions, innermost first, 128-byte-swizzled boxes.  The
+// encoder is a driver call and wants a current context, which a host thread has only after
+// a runtime call that needs one: such a thread gets the current device's and tries again.
+static bool encode_bf16(CUtensorMap* m, const void* ptr, int rank, const cuuint64_t* dims,
+                        const cuuint64_t* strides, const cuuint32_t* box) {
+  PFN_encodeTiled enc = get_encode_tiled();
+  if (!enc) return false;
+  const cuuint32_t estr[3] = {1, 1, 1};
+  auto encode = [&]() {
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, static_cast<cuuint32_t>(rank),
+               const_cast<void*>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  };
+  CUresult r = encode();
+  int dev = 0;
+  if (r == CUDA_ERROR_INVALID_CONTEXT && cudaGetDevice(&dev) == cudaSuccess &&
+      cudaSetDevice(dev) == cudaSuccess)
+    r = encode();
+  return r == CUDA_SUCCESS;
+}
+
 // 2-D bf16 tensor [rows, inner] (inner contiguous), box [box_rows, 64], 128-byte swizzle.
 static bool make_tmap_bf16(CUtensorMap* m, const void* ptr, uint64_t inner, uint64_t rows,
                            uint32_t box_rows) {
-  PFN_encodeTiled enc = get_encode_tiled();
-  if (!enc) return false;
-  cuuint64_t dims[2] = {inner, rows};
-  cuuint64_t strides[1] = {inner * 2};
-  cuuint32_t box[2] = {64, box_rows};
-  cuuint32_t estr[2] = {1, 1};
-  const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(ptr), dims,
-                         strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS;
+  const cuuint64_t dims[2] = {inner, rows};
+  const cuuint64_t strides[1] = {inner * 2};
+  const cuuint32_t box[2] = {64, box_rows};
+  return encode_bf16(m, ptr, 2, dims, strides, box);
 }
 
 // Contiguous bf16 tensor of `rank` (2 or 3) dimensions, innermost first, 128-byte
 // swizzled boxes 64 elements wide.
 bool encode_tmap_bf16(CUtensorMap* m, const void* ptr, int rank, const uint64_t* dims,
                       const uint32_t* box) {
-  PFN_encodeTiled enc = get_encode_tiled();
-  if (!enc) return false;
   cuuint64_t d[3], strides[2];
-  cuuint32_t b[3], estr[3] = {1, 1, 1};
+  cuuint32_t b[3];
   for (int i = 0; i < rank; ++i) {
     d[i] = dims[i];
     b[i] = box[i];
     if (i > 0) strides[i - 1] = (i > 1 ? strides[i - 2] : 2) * dims[i - 1];
   }
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, static_cast<cuuint32_t>(rank),
-             const_cast<void*>(ptr), d, strides, b, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  return encode_bf16(m, ptr, rank, d, strides, b);
 }
 
 static int num_sms_current() {
