@@ -485,8 +485,10 @@ cudaError_t launch_grouped_sm100(const GroupedShape& s, const GroupedPlan& p, Gr
   auto* kernel = which == kGroupedFwd  ? grouped_sm100_kernel<kGroupedFwd>
                  : which == kGroupedDx ? grouped_sm100_kernel<kGroupedDx>
                                        : grouped_sm100_kernel<kGroupedDw>;
+  // the limit holds for the process: always the same value, so that a call of another
+  // shape in another thread cannot lower it between here and the launch
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             static_cast<int>(smem));
+                                             static_cast<int>(kSmemLimit));
   if (e != cudaSuccess) return e;
   const int64_t pairs = num_sms / 2;
   count_launch();

@@ -103,3 +103,21 @@ def test_first_call_of_a_thread():
         job()
         torch.cuda.synchronize()
         assert torch.equal(got["out"], first)
+
+
+@pytest.mark.parametrize("backward", [False, True], ids=["y", "dW"])
+def test_grouped_products_of_different_shapes(backward):
+    torch.cuda.synchronize()
+    # tiles of 64 and of 256 rows; dW with narrow and with wide columns
+    jobs = [_products(10 * i, *((([20] * 4, 64, 64) if i % 2 else ([250, 60], 256, 64))), backward)
+            for i in range(6)]
+    torch.cuda.synchronize()
+    want = []
+    for job, out, _ in jobs:
+        job()
+        torch.cuda.synchronize()
+        want.append(out.clone())
+    assert _at_once([j for j, _, _ in jobs], 4000) == []
+    for (_, out, ws), w in zip(jobs, want):
+        assert swl.lib().switch_layer_device_status(ws.data_ptr(), None) == 0
+        assert torch.equal(out, w)
