@@ -843,8 +843,10 @@ cudaError_t launch_expert_ffn_bf16(const Shape& s, const Workspace& ws, const CU
   auto kern = a.glu ? expert_ffn_sm100_kernel<true, false>
                     : (a.split > 1 ? expert_ffn_sm100_kernel<false, true>
                                    : expert_ffn_sm100_kernel<false, false>);
+  // the limit is the process's: always the most, so that a call of another shape in another
+  // thread cannot lower it between here and the launch
   cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(smem));
+                                         static_cast<int>(kMaxSmem));
   if (err != cudaSuccess) return err;
   err = launch_dependent(kern, dim3(num_sms), dim3(kThreads), smem, stream, tmA1, tmB1, tmA2,
                          tmB2, a);

@@ -1229,8 +1229,10 @@ cudaError_t launch_softmax_t(const Shape& s, const Workspace& ws, const float* b
   const size_t smem = (size_t)(kSoftmaxWarps + 1) * s.N * sizeof(float);
   auto kern = s.topk == 2 ? router_softmax_kernel<NPL, true> : router_softmax_kernel<NPL, false>;
   if (smem > 48 * 1024) {
+    // the limit is the process's: the kernel's most (N = 32 NPL), whatever this call takes
+    constexpr size_t most = (size_t)(kSoftmaxWarps + 1) * 32 * NPL * sizeof(float);
     const cudaError_t e =
-        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
     if (e != cudaSuccess) return e;
   }
   return launch_dependent(kern, dim3(s.nblk), dim3(kSoftmaxThreads), smem, stream,
@@ -1416,8 +1418,10 @@ cudaError_t launch_stream_t(const Shape& s, const Workspace& ws, const float* b_
   auto kern = s.topk == 2 ? router_softmax_stream_kernel<V4, WPR, true, false>
                           : (full ? router_softmax_stream_kernel<V4, WPR, false, true>
                                   : router_softmax_stream_kernel<V4, WPR, false, false>);
+  // the limit is the process's: the kernel's most, whatever this call takes
+  constexpr size_t most = stream_softmax_smem(1024 * WPR);
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(smem));
+                                       static_cast<int>(most));
   if (e != cudaSuccess) return e;
   int dev = 0, sms = 0;
   if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;

@@ -678,7 +678,7 @@ router_logits_wide_kernel(const __grid_constant__ CUtensorMap tmX,
 }
 
 template <int NP>
-size_t tc_smem_bytes(int stages) {
+constexpr size_t tc_smem_bytes(int stages) {
   return 1024 + static_cast<size_t>(stages) * TcCfg<NP>::kStage +
          (2 * kMaxStages + 2) * sizeof(uint64_t) + 2 * sizeof(uint32_t);
 }
@@ -689,9 +689,14 @@ size_t tc_smem_bytes(int stages) {
 // once; each CTA's prologue and routing tail then overlap the other CTA's loads
 // instead of forming a second wave.
 template <int NP>
-int tc_stages(const Shape& s, int num_sms) {
+constexpr int tc_most_stages() {
   int stages = kMaxStages;
   while (stages > 2 && tc_smem_bytes<NP>(stages) > kMaxDynSmem) --stages;
+  return stages;
+}
+template <int NP>
+int tc_stages(const Shape& s, int num_sms) {
+  int stages = tc_most_stages<NP>();
   const int64_t t_tiles = (s.T + kBM - 1) / kBM;
   if (s.ksplit_eff == 1 && 3 * NP <= 256 && t_tiles > num_sms) stages = 2;
   return stages;
@@ -726,8 +731,10 @@ cudaError_t launch_tc_t(const Shape& s, const Workspace& ws, const CUtensorMap& 
   if (ps_bytes > static_cast<size_t>(stages) * TcCfg<NP>::kStage) return cudaErrorInvalidValue;
   a.stages = stages;
   const size_t smem = tc_smem_bytes<NP>(stages);
+  // the limit is the process's: the kernel's most, whatever this call takes
+  constexpr size_t most = tc_smem_bytes<NP>(tc_most_stages<NP>());
   cudaError_t e = cudaFuncSetAttribute(router_tc_kernel<NP>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(t_tiles, 1, static_cast<unsigned>(s.ksplit_eff));

@@ -121,3 +121,19 @@ def test_grouped_products_of_different_shapes(backward):
     for (_, out, ws), w in zip(jobs, want):
         assert swl.lib().switch_layer_device_status(ws.data_ptr(), None) == 0
         assert torch.equal(out, w)
+
+
+def test_layers_of_different_shapes():
+    """A many-expert layer (streaming softmax), a small one (fused router of two stages) and
+    one of few tokens."""
+    jobs = [_layer(1, 512, 64, 64, 600, 1.0), _layer(11, 40000, 64, 64, 8, 1.25),
+            _layer(21, 300, 128, 128, 6, 1.25), _layer(31, 256, 64, 64, 1600, 1.0)]
+    torch.cuda.synchronize()
+    want = []
+    for job, got in jobs:
+        job()
+        torch.cuda.synchronize()
+        want.append(got["out"].clone())
+    assert _at_once([j for j, _ in jobs], 400) == []
+    for (_, got), w in zip(jobs, want):
+        assert torch.equal(got["out"], w)
