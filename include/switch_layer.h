@@ -354,9 +354,10 @@ swl_status switch_layer_norm_residual_backward(int64_t T, int64_t d, int dtype, 
  * bytes and m_scale, v_scale are fp32 [ceil(n / SWL_ADAMW_BLOCK)], one per block
  * of SWL_ADAMW_BLOCK consecutive elements: m = e4m3(m[i]) * m_scale, sqrt(v) =
  * e4m3(v[i]) * v_scale, each scale the block's largest magnitude over 448.  m is
- * rounded to nearest; sqrt(v) is rounded stochastically to e4m3's three mantissa
- * bits with bits drawn from (element, t, seed), so the same call gives the same
- * result; a non-zero sqrt(v) keeps at least the smallest code, and a block whose
+ * rounded to nearest; sqrt(v) is rounded stochastically to one of the two e4m3 codes
+ * next to it with bits drawn from (element, t, seed), so the same call gives the same
+ * result; a non-zero sqrt(v) keeps at least the smallest code, 2^-9 of the scale (below
+ * it, it is held as that, whatever its gradients do), and a block whose
  * largest magnitude is under 2^-100 is held as zeros.  All-zero bytes and scales
  * are the zero state.  The step itself uses the unrounded m and v.
  * A gradient that is not finite makes its element's states and weight not finite

@@ -17,8 +17,9 @@
 // times the scale, rounded to nearest (its moving average renews a tenth of it
 // per step, more than the format's step).  v is held by its root: r = sqrt(v) has
 // half the exponent range, so e4m3's 2^-9..448 spans 35 binary orders of v.  The
-// root is rounded stochastically to its three mantissa bits with 16 random bits
-// per element: with b2 near 1 a step changes r by far less than half a spacing,
+// root is rounded stochastically to the codes next to it (three mantissa bits; from
+// 2^-6 of the scaled value down, where e4m3 has one spacing, multiples of 2^-9) with 16
+// random bits per element: with b2 near 1 a step changes r by far less than half a spacing,
 // and rounding to nearest would never let v move.  The bits come from a
 // counter (element pair, step, seed) through two multiply-xorshift rounds, so a
 // step can be repeated exactly.  A non-zero r keeps at least the smallest code, so
@@ -55,6 +56,8 @@ constexpr int kAdamBlock = SWL_ADAMW_BLOCK;         // elements that share a sca
 constexpr int kChunkBlocks = kAdamWarps;            // blocks a CTA takes at a time
 constexpr int kTableMax = 160;                      // tensors per launch (parameter space)
 constexpr float kLeast = 7.888609052210118e-31f;    // 2^-100
+constexpr float kSubnormal = 0.015625f;             // 2^-6: e4m3 below it has one spacing,
+constexpr float kSmallest = 0.001953125f;           // 2^-9
 
 struct AdamwEntry {
   void* p;
@@ -132,6 +135,19 @@ __device__ __forceinline__ unsigned mix(unsigned x) {
   x = (x ^ (x >> 16)) * 0x6A09E667u;
   x = (x ^ (x >> 15)) * 0xBB67AE85u;
   return x ^ (x >> 16);
+}
+
+// The scaled root q as one of the two codes next to it, the upper one with the probability
+// of what is cut: `bits` are 16 random bits over the cut ones.  Under 2^-6 the codes are
+// 2^-9 apart, as numbers of three mantissa bits are from 2^-6 to 2^-5: rounded there and
+// moved back.
+__device__ __forceinline__ float root_code(float q, unsigned bits) {
+  const bool low = q < kSubnormal;
+  float x = q;
+  if (low) x = __fadd_rn(x, kSubnormal);
+  x = __uint_as_float((__float_as_uint(x) + (bits << 4) + 8u) & 0xfff00000u);
+  if (low) x = fmaxf(__fsub_rn(x, kSubnormal), kSmallest);
+  return q <= 0.f ? 0.f : x;
 }
 
 // Four consecutive elements as they lie in memory: float4 (fp32), uint2 (bf16) or
@@ -321,10 +337,7 @@ struct Block {
           const unsigned u = mix(static_cast<unsigned>((i0 + j) >> 1) + R.key);
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            const float q = __fmul_rn(fv[h][j + k], ir);
-            const unsigned t = (__float_as_uint(q) + ((k ? u >> 16 : u & 0xffffu) << 4) + 8u) &
-                               0xfff00000u;
-            x[j + k] = q <= 0.f ? 0.f : max_nan(__uint_as_float(t), 0.001953125f);
+            x[j + k] = root_code(__fmul_rn(fv[h][j + k], ir), k ? u >> 16 : u & 0xffffu);
             fm[h][j + k] = __fmul_rn(fm[h][j + k], im);
           }
         }
@@ -343,7 +356,8 @@ struct Block {
 // before the current one is worked on, so that the loads overlap the arithmetic
 // (a warp issues about 75 instructions per element of an 8-bit state; measured on
 // 202 M bf16 parameters with masters and 8-bit states: 722 -> 635 us in a run of calls,
-// 566 us alone, 5.7 TB/s).
+// 574 us alone, 5.6 TB/s; 566 with roots rounded to three mantissa bits everywhere, which
+// never moves one of a few 2^-9).
 template <typename P, bool kMaster, bool kEight>
 __device__ __forceinline__ void step_tensor(const AdamwEntry& e, long long b, long long stride,
                                             const Rates& R) {
