@@ -267,7 +267,9 @@ swl_status switch_layer_forward_variant(int64_t T, int64_t d, int64_t d_ff, int6
  * only); outputs are written, not added to.  Outputs and workspace overlap neither inputs
  * nor each other (SWL_ERR_INVALID_ARG).  bf16 requires K % 8 == 0, O % 8 == 0 and 16-byte
  * aligned x, y, W, dy, dx, dW (SWL_ERR_UNSUPPORTED), as the layer does.  workspace:
- * switch_layer_grouped_workspace_size bytes, 256-byte aligned, no initialisation. */
+ * switch_layer_grouped_workspace_size bytes, 256-byte aligned, no initialisation; the
+ * size never falls as R grows, so one for the largest batch serves smaller ones.  Two
+ * calls that share a workspace must not overlap on the GPU. */
 swl_status switch_layer_grouped_workspace_size(int64_t R, int64_t K, int64_t O, int64_t N,
                                                int dtype, size_t* bytes);
 swl_status switch_layer_grouped_matmul(int64_t R, int64_t K, int64_t O, int64_t N, int dtype,

@@ -285,8 +285,10 @@ size_t grouped_layout(const GroupedShape& s, uintptr_t base, GroupedPlan* p) {
   q.tile_prefix = reinterpret_cast<int*>(take((static_cast<size_t>(s.N) + 1) * 4));
   q.maps = reinterpret_cast<void*>(
       take(s.dtype == SWL_BF16 ? static_cast<size_t>(s.N) * 2 * sizeof(CUtensorMap) : 0));
-  q.bias_part = reinterpret_cast<float*>(
-      take((static_cast<size_t>(s.R) / tile_rows(s) + s.N) * static_cast<size_t>(s.O) * 4));
+  // for any call of up to R rows: a program sizes its workspace by the largest batch
+  const int64_t tiles = s.dtype == SWL_BF16 ? grouped_sm100_most_tiles(s)
+                                            : s.R / grouped_f32_tile_rows() + s.N;
+  q.bias_part = reinterpret_cast<float*>(take(static_cast<size_t>(tiles) * s.O * 4));
   if (p) *p = q;
   return at;
 }

@@ -42,6 +42,8 @@ cudaError_t launch_grouped_f32(const GroupedShape& s, const GroupedPlan& p, Grou
 // The same of bf16 tensors; templates: dW's maps for the plan.
 bool grouped_sm100_templates(const GroupedShape& s, const void* dy, const void* x, CUtensorMap* out);
 int grouped_sm100_tile_rows(const GroupedShape& s);
+// Row tiles of a call with up to R rows, at most (fewer rows may take smaller tiles).
+int64_t grouped_sm100_most_tiles(const GroupedShape& s);
 cudaError_t launch_grouped_sm100(const GroupedShape& s, const GroupedPlan& p, GroupedWhich which,
                                  const int* offsets, const void* a, const void* b,
                                  const void* bias, void* out, int num_sms, cudaStream_t stream);

@@ -432,6 +432,10 @@ bool grouped_sm100_templates(const GroupedShape& s, const void* dy, const void* 
 // spread unevenly: 24 per group 95 us with 256 and 90 with 64, 40: 99 and 99, 64: 104
 // and 117, 96: 110 and 166.
 int grouped_sm100_tile_rows(const GroupedShape& s) { return s.R >= 40 * s.N ? 256 : 64; }
+int64_t grouped_sm100_most_tiles(const GroupedShape& s) {
+  const int64_t few = (s.R < 40 * s.N ? s.R : 40 * s.N - 1) / 64, all = s.R / grouped_sm100_tile_rows(s);
+  return (few > all ? few : all) + s.N;
+}
 
 cudaError_t launch_grouped_sm100(const GroupedShape& s, const GroupedPlan& p, GroupedWhich which,
                                  const int* offsets, const void* a, const void* b,

@@ -137,3 +137,21 @@ def test_products_behind_a_norm_that_sums_no_columns(dtype):
         dy = swl.norm_residual_backward(dr, None, y, y=y, gate=gate)["dy"]
         got = swl.grouped_matmul(dy, off, W, out=torch.zeros_like(product), check=False)
         assert torch.equal(dy, want) and torch.equal(got, product)
+
+
+def test_a_workspace_for_the_largest_batch_serves_smaller_ones():
+    N, K, O = 16, 64, 136
+    g = torch.Generator(device="cuda").manual_seed(12)
+    x, dy = _n(g, (40 * N, K), BF), _n(g, (40 * N, O), BF)
+    W = _n(g, (N, O, K), BF, K ** -0.5)
+    ws = torch.empty(swl.switch_layer_grouped_workspace_size(40 * N, K, O, N, swl.SWL_BF16),
+                     dtype=torch.uint8, device="cuda")
+    for rows in (40 * N, 40 * N - 1, 39 * N, 100, 1):
+        off = _offsets([rows // 2] + [0] * (N - 2) + [rows - rows // 2])
+        args = dy[:rows], x[:rows], off, W
+        got = swl.grouped_matmul_backward(*args, workspace=ws)
+        want = swl.grouped_matmul_backward(*args)
+        for k in want:
+            assert torch.equal(got[k], want[k]), (rows, k)
+        assert torch.equal(swl.grouped_matmul(x[:rows], off, W, workspace=ws),
+                           swl.grouped_matmul(x[:rows], off, W))
