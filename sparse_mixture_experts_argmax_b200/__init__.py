@@ -837,7 +837,9 @@ def _allocating_on(stream, dev: torch.device):
     if stream is None:
         return _HERE_ALREADY
     if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream), device=dev)
+        h = int(stream)          # 0 and 1 are both the legacy default stream
+        stream = (torch.cuda.default_stream(dev) if h in (0, 1) else
+                  torch.cuda.ExternalStream(h, device=dev))
     return torch.cuda.stream(stream)
 
 

@@ -155,3 +155,25 @@ def test_a_workspace_for_the_largest_batch_serves_smaller_ones():
             assert torch.equal(got[k], want[k]), (rows, k)
         assert torch.equal(swl.grouped_matmul(x[:rows], off, W, workspace=ws),
                            swl.grouped_matmul(x[:rows], off, W))
+
+
+def test_streams_given_as_handles():
+    """0 and 1 are the legacy default stream's handles, 2 the calling thread's default stream."""
+    g = torch.Generator(device="cuda").manual_seed(13)
+    x, W, off = _n(g, (40, 64), F), _n(g, (2, 24, 64), F), _offsets([10, 30])
+    w = torch.ones(64, device="cuda")
+    want = swl.grouped_matmul(x, off, W)
+    wantg = swl.grouped_matmul_backward(want, x, off, W)
+    norm = swl.norm_residual(x, w_pre=w)
+    back = swl.norm_residual_backward(None, x, x, w_pre=w)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for handle in (0, 1, 2, side.cuda_stream):
+        y = swl.grouped_matmul(x, off, W, stream=handle)
+        gr = swl.grouped_matmul_backward(want, x, off, W, stream=handle)
+        nr = swl.norm_residual(x, w_pre=w, stream=handle)
+        nb = swl.norm_residual_backward(None, x, x, w_pre=w, stream=handle)
+        torch.cuda.synchronize()
+        assert torch.equal(y, want) and torch.equal(nr["h"], norm["h"]), handle
+        assert all(torch.equal(gr[k], wantg[k]) for k in wantg), handle
+        assert torch.equal(nb["dx"], back["dx"]) and torch.equal(nb["dw_pre"], back["dw_pre"]), handle
