@@ -246,9 +246,16 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
     return None if t is None else t.data_ptr()
 
 
+# torch's own short ways to the current device and its stream's handle make no Stream object;
+# they are not public, so under a torch without them the public ones stand in.
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda device: torch.cuda.current_stream(device).cuda_stream)
+
+
 def _stream_handle(stream) -> int:
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        return _raw_stream(_current_device())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
@@ -826,7 +833,7 @@ _HERE_ALREADY = contextlib.nullcontext()
 
 def _on(dev: torch.device):
     """A context in which ``dev`` is the current device (the library launches there)."""
-    if dev.index is None or dev.index == torch._C._cuda_getDevice():
+    if dev.index is None or dev.index == _current_device():
         return _HERE_ALREADY
     return torch.cuda.device(dev)
 
