@@ -621,7 +621,8 @@ int switch_layer_router_mode(void);
  * another CTA's hidden rows) gives up after a time limit, sets the device
  * status to SWL_ERR_DEVICE and lets the kernel drain and return, so the CUDA
  * context stays usable.  switch_layer_set_wait_limit_ns sets that limit (0
- * restores the default of 2 s).  switch_layer_set_stall_test(1) makes the
+ * restores the default of 2 s; the grouped products add 20 us for every 64 terms of a
+ * sum, as a wait of theirs may last that long).  switch_layer_set_stall_test(1) makes the
  * expert FFN wait for one GEMM1 epilogue warp more than token tile 0 has, a
  * signal that never comes: the wait runs out after the limit and the call
  * reports SWL_ERR_DEVICE through switch_layer_device_status (outputs of that

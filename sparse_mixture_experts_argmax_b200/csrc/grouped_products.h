@@ -31,6 +31,13 @@ enum GroupedWhich : int { kGroupedFwd = 0, kGroupedDx = 1, kGroupedDw = 2 };
 cudaError_t launch_grouped_plan(const GroupedShape& s, const GroupedPlan& p, const int* offsets,
                                 int tile_rows, cudaStream_t stream);
 
+// Bound of a kernel's waits: some last for a whole tile, whose steps go 64 deep along the
+// summed axis (2^30 rows of one group in dW, at most), so the limit grows with them:
+// 20 us a step, of which the slowest (fp32) takes 2.2.
+inline unsigned long long grouped_wait_ns(int64_t depth) {
+  return wait_limit_ns() + 20000ull * static_cast<unsigned long long>((depth + 63) / 64);
+}
+
 // The products of fp32 tensors.  which: y = x W^T + b (kGroupedFwd: a = x, b = W,
 // bias), dx = dy W (kGroupedDx: a = dy, b = W) or dW = dy^T x (kGroupedDw: a = dy, b = x;
 // every group written, empty ones zero).

@@ -507,7 +507,7 @@ cudaError_t launch_grouped_f32(const GroupedShape& s, const GroupedPlan& p, Grou
   g.bias = static_cast<const float*>(bias);
   g.out = static_cast<float*>(out);
   g.hdr = p.hdr;
-  g.wait_ns = wait_limit_ns();
+  g.wait_ns = grouped_wait_ns(which == kGroupedFwd ? s.K : which == kGroupedDx ? s.O : s.R);
   g.O = static_cast<int>(s.O);
   g.K = static_cast<int>(s.K);
   g.shape.off = offsets;

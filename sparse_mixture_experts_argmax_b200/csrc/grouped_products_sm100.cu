@@ -450,7 +450,7 @@ cudaError_t launch_grouped_sm100(const GroupedShape& s, const GroupedPlan& p, Gr
   g.maps = static_cast<const CUtensorMap*>(p.maps);
   g.bias = static_cast<const __nv_bfloat16*>(bias);
   g.out = static_cast<__nv_bfloat16*>(out);
-  g.wait_ns = wait_limit_ns();
+  g.wait_ns = grouped_wait_ns(which == kGroupedFwd ? s.K : which == kGroupedDx ? s.O : s.R);
   g.shape.N = static_cast<int>(N);
   int64_t tiles;      // at most
   if (which == kGroupedDw) {
