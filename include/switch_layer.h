@@ -255,9 +255,13 @@ swl_status switch_layer_forward_variant(int64_t T, int64_t d, int64_t d_ff, int6
  *   dx[r] = W[e]^T dy[r],  dW[e] = sum_r dy[r] x[r]^T,  db[e] = sum_r dy[r]
  *   R, K, O, N   rows of the buffers (R = 0: no rows), width of x, width of y, groups
  *   x [R, K], y [R, O], W [N, O, K], bias [N, O] or NULL: dtype; sums are fp32, each result
- *                rounded once.  fp32 products are eight bf16 products of exact three-piece
- *                splits (under 2^-28 of a product is left out); a sum with an infinite
- *                or NaN factor is not finite (NaN where fp32 arithmetic gives infinity)
+ *                rounded once.  y of up to 32 fp32 rows: plain fp32 sums.  Other fp32
+ *                products are eight bf16 products of three-piece splits (under 2^-28 of a
+ *                product is left out).  The split is exact for numbers of 2^-110 and more
+ *                and for zero; a smaller one is taken to within 2^-133, which matters beside a
+ *                factor so large that the product is of ordinary size.  A sum with an
+ *                infinite or NaN factor is not finite: as fp32 arithmetic gives it for up to
+ *                32 rows of y, NaN elsewhere
  *   offsets      DEVICE int32 [N + 1], 0 <= offsets[0] <= ... <= offsets[N] <= R.  Rows
  *                outside every group are neither read nor written: y and dx keep them.
  *                Empty groups: no rows, and zero dW and db.

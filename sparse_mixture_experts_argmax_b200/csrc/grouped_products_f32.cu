@@ -1,9 +1,10 @@
 // Products grouped by expert on the tensor cores for fp32 tensors: y = x W^T + b,
 // dx = dy W and dW = dy^T x over ragged row ranges.
 //
-// An fp32 number is the sum of three bf16 numbers exactly: its leading 8 significant
-// bits, the next 8 and the last 8 (x = hi + mid + lo, cut, not rounded: two instructions
-// a piece, and nothing overflows; of a number that is not finite a rest is NaN).  A
+// An fp32 number is the sum of three bf16 numbers: its leading 8 significant bits, the
+// next 8 and the last 8 (x = hi + mid + lo, cut, not rounded: two instructions a piece,
+// and nothing overflows; of a number that is not finite a rest is NaN).  Exactly so from
+// 2^-110 on; bf16 ends at 2^-133, and what a smaller number has below that is cut off.  A
 // product is then eight bf16 products, each exact in fp32,
 //   lo mid' + mid lo' + lo hi' + hi lo' + mid mid' + mid hi' + hi mid' + hi hi',
 // the ninth, lo lo', being under 2^-28 of it.  Eight tensor-core products cost 0.2 of
