@@ -353,14 +353,19 @@ swl_status switch_layer_norm_residual_backward(int64_t T, int64_t d, int dtype, 
  *   m = beta1 m + (1 - beta1) g,   v = beta2 v + (1 - beta2) g^2
  *   w = w (1 - lr' weight_decay)
  *       - lr' / (1 - beta1^t) * m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
- * in fp32 (bias corrections in fp64), each operation rounded on its own.  w is the
- * parameter, or its fp32 master copy when there is one (bf16 parameters only): the
- * parameter is then written, rounded from w, and not read.
+ * in fp32 (bias corrections in fp64).  m and v: each operation is rounded on its own, so
+ * that 8-bit codes are a fixed function of the inputs.  w: fused multiply-adds, a division
+ * to two units of the last place and, with 32-bit states, a square root to one (the
+ * update is within 16 2^-24 of itself).  w is the parameter, or its fp32 master copy when
+ * there is one (bf16 parameters only): the parameter is then written, rounded from w, and
+ * not read.
  * States: state_bits = 32: m and v are fp32 [n].  state_bits = 8: m and v are [n]
  * bytes and m_scale, v_scale are fp32 [ceil(n / SWL_ADAMW_BLOCK)], one per block
  * of SWL_ADAMW_BLOCK consecutive elements: m = e4m3(m[i]) * m_scale, sqrt(v) =
  * e4m3(v[i]) * v_scale, each scale the block's largest magnitude over 448.  m is
- * rounded to nearest; sqrt(v) is rounded stochastically to one of the two e4m3 codes
+ * rounded to nearest, so a step that would move it by less than half a spacing (3 to 6% of
+ * it; 2^-10 of the scale at least) leaves it: beta1 = 0.9 moves by a tenth of g - m, a
+ * larger beta1 leaves more of a changed gradient out; sqrt(v) is rounded stochastically to one of the two e4m3 codes
  * next to it with bits drawn from (element, t, seed), so the same call gives the same
  * result; a non-zero sqrt(v) keeps at least the smallest code, 2^-9 of the scale (below
  * it, it is held as that, whatever its gradients do), and a block whose

@@ -15,7 +15,7 @@
 // 8-bit states: blocks of 256 consecutive elements share an fp32 scale, the
 // largest magnitude over 448 (the largest e4m3 number).  m is held as e4m3
 // times the scale, rounded to nearest (its moving average renews a tenth of it
-// per step, more than the format's step).  v is held by its root: r = sqrt(v) has
+// per step with beta1 = 0.9, more than half a spacing; with a larger beta1 less).  v is held by its root: r = sqrt(v) has
 // half the exponent range, so e4m3's 2^-9..448 spans 35 binary orders of v.  The
 // root is rounded stochastically to the codes next to it (three mantissa bits; from
 // 2^-6 of the scaled value down, where e4m3 has one spacing, multiples of 2^-9) with 16

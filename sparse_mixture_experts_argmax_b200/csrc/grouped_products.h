@@ -27,9 +27,9 @@ enum GroupedWhich : int { kGroupedFwd = 0, kGroupedDx = 1, kGroupedDw = 2 };
 
 // Reads and checks the offsets (0 <= off[0] <= ... <= off[N] <= R), counts the row
 // tiles and resets the header.  Bad offsets: kDevIndexOutOfRange and no tiles, so
-// that the kernels behind it touch nothing.
+// that the kernels behind it touch nothing.  maps: dW's two templates, or NULL.
 cudaError_t launch_grouped_plan(const GroupedShape& s, const GroupedPlan& p, const int* offsets,
-                                int tile_rows, cudaStream_t stream);
+                                int tile_rows, const CUtensorMap* maps, cudaStream_t stream);
 
 // Bound of a kernel's waits: some last for a whole tile, whose steps go 64 deep along the
 // summed axis (2^30 rows of one group in dW, at most), so the limit grows with them:

@@ -7,7 +7,7 @@
 // 2^-110 on; bf16 ends at 2^-133, and what a smaller number has below that is cut off.  A
 // product is then eight bf16 products, each exact in fp32,
 //   lo mid' + mid lo' + lo hi' + hi lo' + mid mid' + mid hi' + hi mid' + hi hi',
-// the ninth, lo lo', being under 2^-28 of it.  Eight tensor-core products cost 0.2 of
+// the ninth, lo lo', being under 2^-28 of it.  Eight tensor-core products cost 0.37 of
 // one fp32 FMA per term at these units' rates (1.64 PFLOP/s against 75 TFLOP/s).  Six
 // products of pieces rounded to nearest leave out 2^-23, and the rounding cost more than
 // the two products.
