@@ -295,7 +295,9 @@ swl_status switch_layer_grouped_matmul_backward(int64_t R, int64_t K, int64_t O,
  *   h_t = n(r_t; w_pre, b_pre)             the next block's input
  * x is the residual stream, y the block's output (for this layer: out, zero rows for
  * dropped tokens; for experts run with the grouped products: the combined rows, with
- * gate the router's).  y NULL: only h = n(x); then r is NULL.  h NULL (and w_pre
+ * gate the router's).  out is multiplied by the layer's gate already: n(out; w_post)
+ * would take that factor out, and the router's gradient through the layer with it, so
+ * w_post goes with ungated rows and gate.  y NULL: only h = n(x); then r is NULL.  h NULL (and w_pre
  * NULL): no second norm.  Sums and statistics are fp32; r and h are each rounded
  * once (h is taken from the unrounded r).
  *   x, y, r, h      [T, d] of dtype; r and h may be x or y themselves (in place), but
@@ -365,11 +367,11 @@ swl_status switch_layer_norm_residual_backward(int64_t T, int64_t d, int dtype, 
  * e4m3(v[i]) * v_scale, each scale the block's largest magnitude over 448.  m is
  * rounded to nearest, so a step that would move it by less than half a spacing (3 to 6% of
  * it; 2^-10 of the scale at least) leaves it: beta1 = 0.9 moves by a tenth of g - m, a
- * larger beta1 leaves more of a changed gradient out; sqrt(v) is rounded stochastically to one of the two e4m3 codes
- * next to it with bits drawn from (element, t, seed), so the same call gives the same
- * result; a non-zero sqrt(v) keeps at least the smallest code, 2^-9 of the scale (below
- * it, it is held as that, whatever its gradients do), and a block whose
- * largest magnitude is under 2^-100 is held as zeros.  All-zero bytes and scales
+ * larger beta1 leaves more of a changed gradient out.  sqrt(v) is rounded stochastically
+ * to one of the two e4m3 codes next to it with bits drawn from (element, t, seed), so the
+ * same call gives the same result; a non-zero sqrt(v) keeps at least the smallest code,
+ * 2^-9 of the scale (below it, it is held as that, whatever its gradients do).  A block
+ * whose largest magnitude is under 2^-100 is held as zeros.  All-zero bytes and scales
  * are the zero state.  The step itself uses the unrounded m and v.
  * A gradient that is not finite makes its element's states and weight not finite
  * (8-bit states: the states of its whole block).

@@ -12,19 +12,19 @@
 // parameters are rounded from w once; with an fp32 master copy w is read from
 // and kept there, and the bf16 parameter is only written.
 //
-// 8-bit states: blocks of 256 consecutive elements share an fp32 scale, the
-// largest magnitude over 448 (the largest e4m3 number).  m is held as e4m3
-// times the scale, rounded to nearest (its moving average renews a tenth of it
-// per step with beta1 = 0.9, more than half a spacing; with a larger beta1 less).  v is held by its root: r = sqrt(v) has
-// half the exponent range, so e4m3's 2^-9..448 spans 35 binary orders of v.  The
-// root is rounded stochastically to the codes next to it (three mantissa bits; from
-// 2^-6 of the scaled value down, where e4m3 has one spacing, multiples of 2^-9) with 16
-// random bits per element: with b2 near 1 a step changes r by far less than half a spacing,
-// and rounding to nearest would never let v move.  The bits come from a
-// counter (element pair, step, seed) through two multiply-xorshift rounds, so a
-// step can be repeated exactly.  A non-zero r keeps at least the smallest code, so
-// no element's denominator falls to eps alone; a block whose largest magnitude is
-// under 2^-100 is held as zeros.  The step itself uses the unrounded m and v.
+// 8-bit states: blocks of 256 consecutive elements share an fp32 scale, the largest
+// magnitude over 448 (the largest e4m3 number).  m is held as e4m3 times the scale, rounded
+// to nearest (its moving average renews a tenth of it per step with beta1 = 0.9, more than
+// half a spacing; with a larger beta1 less).  v is held by its root: r = sqrt(v) has half
+// the exponent range, so e4m3's 2^-9..448 spans 35 binary orders of v.  The root is rounded
+// stochastically to the codes next to it (three mantissa bits; from 2^-6 of the scaled
+// value down, where e4m3 has one spacing, multiples of 2^-9) with 16 random bits per
+// element: with b2 near 1 a step changes r by far less than half a spacing, and rounding
+// to nearest would never let v move.  The bits come from a counter (element pair, step,
+// seed) through two multiply-xorshift rounds, so a step can be repeated exactly.  A
+// non-zero r keeps at least the smallest code, so no element's denominator falls to eps
+// alone; a block whose largest magnitude is under 2^-100 is held as zeros.  The step itself
+// uses the unrounded m and v.
 //
 // Bound: HBM.  Per element 12 bytes of fp32 weight and gradient (bf16: 6, with a
 // master 12) and 16 bytes of fp32 states or 4.06 of 8-bit ones.  One warp takes one
