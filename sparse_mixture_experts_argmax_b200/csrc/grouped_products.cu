@@ -60,14 +60,16 @@ struct MapPair {
 // CTA 0 counts (a group has at most R / tile_rows + 1 tiles, so the counts fit an int);
 // the others make dW's maps, a warp per group: the templates with the rows ended at
 // the group's last one.  A map's end is clipped to R whatever the offsets say.
-// The trigger follows the wait: what runs behind the plan starts when the call's inputs
-// are complete, so only the plan's own outputs change under it (these it reads by
-// ordinary loads), and its other operands may go through the read-only path.
+// It lets the product start at once (a trigger behind the wait: 653 instead of 638 us for
+// 32768 rows of 64 skewed groups, 2048 -> 5120, call after call), so the kernels behind it
+// may be on the GPU while the call's inputs are still being written: they read all of
+// them, and the plan's results, by ordinary loads or the copy engine, never through the
+// read-only path, which does not promise to see what was written after their start.
 __global__ void __launch_bounds__(kPlanThreads)
 grouped_plan_kernel(const __grid_constant__ PlanArgs a, const __grid_constant__ MapPair templates) {
   __shared__ int warp_sums[32];
-  pdl_wait();
   pdl_trigger();
+  pdl_wait();
   const int* off = a.off;
   int* prefix = a.prefix;
   WsHeader* hdr = a.hdr;
@@ -131,15 +133,14 @@ __device__ __forceinline__ int find_group(const int* P, int N, int q) {
 // interleaved runs of rows (a warp each, 16-byte loads for bf16), then the runs in order.
 // A group of one tile is then done; the tiles of a larger one leave fp32 partial sums
 // that the second kernel adds in order, so a group of many rows is spread over as many
-// CTAs as it has tiles.  Bound: one read of dy.  (prefix and part are written by the
-// kernels just before: ordinary loads.)
+// CTAs as it has tiles.  Bound: one read of dy.
 template <typename T>
 struct BiasVec;
 template <>
 struct BiasVec<__nv_bfloat16> {
   static constexpr int V = 8;
   __device__ static __forceinline__ void add(const __nv_bfloat16* p, float (&s)[V]) {
-    const uint4 q = __ldg(reinterpret_cast<const uint4*>(p));
+    const uint4 q = *reinterpret_cast<const uint4*>(p);
     const unsigned u[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -151,13 +152,13 @@ struct BiasVec<__nv_bfloat16> {
 template <>
 struct BiasVec<float> {
   static constexpr int V = 1;       // any width, any alignment of a float
-  __device__ static __forceinline__ void add(const float* p, float (&s)[V]) { s[0] += __ldg(p); }
+  __device__ static __forceinline__ void add(const float* p, float (&s)[V]) { s[0] += *p; }
 };
 
 template <typename T>
 __global__ void __launch_bounds__(256)
-grouped_bias_tile_kernel(const T* __restrict__ dy, const int* off, const int* prefix, T* db,
-                         float* part, const WsHeader* hdr, int O, int N, int tile_rows) {
+grouped_bias_tile_kernel(const T* dy, const int* off, const int* prefix, T* db, float* part,
+                         const WsHeader* hdr, int O, int N, int tile_rows) {
   constexpr int V = BiasVec<T>::V;
   __shared__ float buf[8][32 * V];
   pdl_trigger();

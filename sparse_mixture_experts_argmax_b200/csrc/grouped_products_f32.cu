@@ -99,17 +99,17 @@ __device__ __forceinline__ void load_run(const float* p, int n, bool even,
                                          float (&v)[Runs<kWide>::kRun]) {
   if constexpr (kWide) {       // n is a multiple of 4
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
-    if (n > 0) a = __ldg(reinterpret_cast<const float4*>(p));
-    if (n > 4) b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+    if (n > 0) a = *reinterpret_cast<const float4*>(p);
+    if (n > 4) b = *(reinterpret_cast<const float4*>(p) + 1);
     v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
     v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
   } else if (even) {           // n is even
     float2 a = make_float2(0.f, 0.f);
-    if (n > 0) a = __ldg(reinterpret_cast<const float2*>(p));
+    if (n > 0) a = *reinterpret_cast<const float2*>(p);
     v[0] = a.x, v[1] = a.y;
   } else {
-    v[0] = n > 0 ? __ldg(p) : 0.f;
-    v[1] = n > 1 ? __ldg(p + 1) : 0.f;
+    v[0] = n > 0 ? *p : 0.f;
+    v[1] = n > 1 ? p[1] : 0.f;
   }
 }
 
