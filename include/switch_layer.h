@@ -255,7 +255,9 @@ swl_status switch_layer_forward_variant(int64_t T, int64_t d, int64_t d_ff, int6
  *   dx[r] = W[e]^T dy[r],  dW[e] = sum_r dy[r] x[r]^T,  db[e] = sum_r dy[r]
  *   R, K, O, N   rows of the buffers (R = 0: no rows), width of x, width of y, groups
  *   x [R, K], y [R, O], W [N, O, K], bias [N, O] or NULL: dtype; sums are fp32, each result
- *                rounded once.  y of up to 32 fp32 rows: plain fp32 sums.  Other fp32
+ *                rounded once.  (bf16: the tensor cores cut their running sums, 2^-23 or
+ *                less of them for every 16 terms; a sum is cut over 32768 terms at most and
+ *                such pieces are added up rounded.)  y of up to 32 fp32 rows: plain fp32 sums.  Other fp32
  *                products are eight bf16 products of three-piece splits (under 2^-28 of a
  *                product is left out).  The split is exact for numbers of 2^-110 and more
  *                and for zero; a smaller one is taken to within 2^-133, which matters beside a
@@ -263,7 +265,8 @@ swl_status switch_layer_forward_variant(int64_t T, int64_t d, int64_t d_ff, int6
  *                infinite or NaN factor is not finite: as fp32 arithmetic gives it for up to
  *                32 rows of y, NaN elsewhere
  *   offsets      DEVICE int32 [N + 1], 0 <= offsets[0] <= ... <= offsets[N] <= R.  Rows
- *                outside every group are neither read nor written: y and dx keep them.
+ *                outside every group have no part in any result and are not written: y
+ *                and dx keep them.
  *                Empty groups: no rows, and zero dW and db.
  * The offsets are only on the device: offsets that break the rule write nothing and
  * make switch_layer_device_status SWL_ERR_DEVICE, as does a pipeline wait that runs out.

@@ -5,7 +5,7 @@
 //   y[r]  = W[e] x[r] + b[e]                  W [N, O, K], b [N, O]
 //   dx[r] = W[e]^T dy[r]
 //   dW[e] = sum_r dy[r] x[r]^T,  db[e] = sum_r dy[r]
-// Rows outside every group are neither read nor written.
+// Rows outside every group have no part in any result and are not written.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -290,6 +290,8 @@ size_t grouped_layout(const GroupedShape& s, uintptr_t base, GroupedPlan* p) {
   const int64_t tiles = s.dtype == SWL_BF16 ? grouped_sm100_most_tiles(s)
                                             : s.R / grouped_f32_tile_rows() + s.N;
   q.bias_part = reinterpret_cast<float*>(take(static_cast<size_t>(tiles) * s.O * 4));
+  q.sums = reinterpret_cast<float*>(
+      take(s.dtype == SWL_BF16 ? grouped_sm100_summing_ctas(s) * kSumsPerCta * 4 : 0));
   if (p) *p = q;
   return at;
 }

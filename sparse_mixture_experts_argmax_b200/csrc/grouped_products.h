@@ -20,6 +20,7 @@ struct GroupedPlan {
   WsHeader* hdr;       // err, next_tile
   int* tile_prefix;    // [N + 1] row tiles of groups before e (tile_rows rows each)
   float* bias_part;    // [row tiles, at most][O] partial bias gradients
+  float* sums;         // bf16 sums of many pieces: a CTA's half of D, [CTA][256][128]
   void* maps;          // bf16: [2 N] tensor maps, dy's and x's rows up to each group's end
 };
 
@@ -49,6 +50,9 @@ cudaError_t launch_grouped_f32(const GroupedShape& s, const GroupedPlan& p, Grou
 // The same of bf16 tensors; templates: dW's maps for the plan.
 bool grouped_sm100_templates(const GroupedShape& s, const void* dy, const void* x, CUtensorMap* out);
 int grouped_sm100_tile_rows(const GroupedShape& s);
+// CTAs whose sums may have to be kept between pieces (0: no sum is that long).
+int grouped_sm100_summing_ctas(const GroupedShape& s);
+constexpr size_t kSumsPerCta = 256 * 128;
 // Row tiles of a call with up to R rows, at most (fewer rows may take smaller tiles).
 int64_t grouped_sm100_most_tiles(const GroupedShape& s);
 cudaError_t launch_grouped_sm100(const GroupedShape& s, const GroupedPlan& p, GroupedWhich which,

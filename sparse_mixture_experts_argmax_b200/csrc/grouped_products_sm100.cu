@@ -19,6 +19,13 @@
 // for dW).  Both come by TMA in 128-byte-swizzled boxes 64 elements wide; no operand
 // is transposed in memory.
 //
+// The tensor cores cut their running sums instead of rounding them: dW of positive terms
+// over one group of 2^16, 2^20 and 2^22 rows came out short by 4e-4, 7e-3 and 2e-2 (half a
+// step of bf16 is 2e-3 to 4e-3).  A sum of more than 32768 terms is therefore made in pieces
+// of so many, a piece a tile of its own in TMEM; the epilogue threads add the pieces up in
+// fp32, rounded, in the workspace (each thread its own numbers, 128 KB per CTA, which stay
+// in L2).
+//
 // Roles of a CTA's 12 warps: 0 and 2 TMA producers of A and B, 1 MMA issuer (first CTA
 // of the pair only), 3 tile decoder, 4-11 epilogue (two warps per lane quarter).  Two
 // 256-column accumulators, so a tile's epilogue runs under the next tile's products.
@@ -34,6 +41,8 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
+
 #include "grouped_products.h"
 #include "grouped_sm100.cuh"
 
@@ -47,6 +56,8 @@ constexpr int kMaxStages = 12;
 constexpr int kAccs = 2;
 constexpr int kTmemCols = 512;
 constexpr int kTileRing = 8;
+constexpr int kPiece = 512;                      // most steps of a sum in TMEM
+constexpr int kSummingPairs = 128;
 // Staging of an epilogue warp: y, dx: 32 rows of 32 features; dW: 32 rows of 64 columns,
 // twice (the next rows are converted while a store reads the last ones).
 template <int W>
@@ -61,6 +72,7 @@ struct Args {
   const CUtensorMap* maps;      // dW: [2 N] maps of dy and x per group
   const __nv_bfloat16* bias;
   __nv_bfloat16* out;
+  float* sums;                  // this launch's CTAs' [256][128] each
   unsigned long long wait_ns;
   int m;           // rows of D per group: O (y, dW) or K (dx); the epilogue's features
   int bn;          // most rows of B per tile
@@ -147,17 +159,25 @@ grouped_sm100_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
   if (warp == 3) {
     // ------------------------------------------------------------ tile decoder
     if (lane == 0) {
-      int t = pair;
-      for (int i = 0;; ++i, t += pairs) {
-        const int slot = i % kTileRing;
-        if (!ptx::mbar_wait(&ring_empty[slot], ((i / kTileRing) & 1) ^ 1u, abort_flag, args.wait_ns)) {
-          fail();
-          break;
-        }
-        const Tile ts = decode_tile<W>(t, total, args.shape);
-        ring[slot] = ts;
-        ptx::mbar_arrive(&ring_full[slot]);
-        if (ts.t < 0) break;
+      bool more = true;
+      for (int i = 0, t = pair; more; t += pairs) {
+        Tile ts = decode_tile<W>(t, total, args.shape);
+        const int steps = ts.kb;
+        more = ts.t >= 0;
+        do {
+          const int slot = i % kTileRing;
+          if (!ptx::mbar_wait(&ring_empty[slot], ((i / kTileRing) & 1) ^ 1u, abort_flag, args.wait_ns)) {
+            fail();
+            more = false;
+            break;
+          }
+          ts.kb = min(steps - ts.k0, kPiece);
+          ts.part = (ts.k0 > 0 ? kAddSum : 0) | (ts.k0 + ts.kb < steps ? kKeepSum : 0);
+          ring[slot] = ts;
+          ptx::mbar_arrive(&ring_full[slot]);
+          ++i;
+          ts.k0 += ts.kb;
+        } while (ts.k0 < steps);
       }
     }
     __syncwarp();
@@ -197,7 +217,7 @@ grouped_sm100_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
         const int m0 = ts.m0 + static_cast<int>(rank) * 128;
         const int b0 = (W == kGroupedDw ? ts.n0 : ts.row0) + static_cast<int>(rank) * half;
         const uint32_t bytes = 2 * (kABytes + static_cast<uint32_t>(half) * kBK * 2);
-        for (int kb = 0; kb < ts.kb; ++kb) {
+        for (int kb = ts.k0; kb < ts.k0 + ts.kb; ++kb) {
           if (!ptx::mbar_wait(&empty[stage], ph ^ 1u, abort_flag, args.wait_ns)) {
             fail();
             ok = false;
@@ -305,6 +325,18 @@ grouped_sm100_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
     int acc = 0;
     uint32_t aph = 0;
     bool flip = false;
+    // this thread's numbers of a sum in pieces: column c at [c][q * 32 + lane]
+    float* const sums = args.sums + static_cast<size_t>(blockIdx.x) * kSumsPerCta + q * 32 + lane;
+    auto join = [&](uint32_t (&r)[32], int c0, int part) {
+#pragma unroll
+      for (int j = 0; j < 32; ++j) {
+        float* const s = sums + (c0 + j) * 128;
+        float v = __uint_as_float(r[j]);
+        if (part & kAddSum) v += *s;
+        if (part & kKeepSum) *s = v;
+        r[j] = __float_as_uint(v);
+      }
+    };
     for (int i = 0;; ++i) {
       const int slot = i % kTileRing;
       if (!__all_sync(0xffffffffu, ptx::mbar_wait(&ring_full[slot], (i / kTileRing) & 1, abort_flag,
@@ -343,6 +375,11 @@ grouped_sm100_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
 #pragma unroll
             for (int j = 0; j < 64; ++j) r[j >> 5][j & 31] = 0u;
           }
+          if (ts.part) {
+            join(r[0], c0, ts.part);
+            join(r[1], c0 + 32, ts.part);
+            if (ts.part & kKeepSum) continue;
+          }
           // this half of the staging is free once the store before the last has read it
           uint8_t* const half_out = stage_out + (flip ? 4096 : 0);
           flip = !flip;
@@ -376,6 +413,10 @@ grouped_sm100_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
           uint32_t r[32];
           ptx::tmem_ld_32x32b_x32(t0 + static_cast<uint32_t>(c0), r);
           ptx::tmem_ld_wait();
+          if (ts.part) {
+            join(r, c0, ts.part);
+            if (ts.part & kKeepSum) continue;
+          }
 #pragma unroll
           for (int j = 0; j < 32; j += 2) {     // two rows per conversion
             const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(r[j]) + bias,
@@ -432,6 +473,12 @@ bool grouped_sm100_templates(const GroupedShape& s, const void* dy, const void* 
 // spread unevenly: 24 per group 95 us with 256 and 90 with 64, 40: 99 and 99, 64: 104
 // and 117, 96: 110 and 166.
 int grouped_sm100_tile_rows(const GroupedShape& s) { return s.R >= 40 * s.N ? 256 : 64; }
+int grouped_sm100_summing_ctas(const GroupedShape& s) {
+  constexpr int64_t most = int64_t{kPiece} * kBK;
+  if (s.K > most || s.O > most) return 2 * kSummingPairs;
+  const int64_t tiles = s.N * ((s.O + 255) / 256) * ((s.K + 255) / 256);      // dW's
+  return s.R <= most ? 0 : static_cast<int>(2 * (tiles < kSummingPairs ? tiles : kSummingPairs));
+}
 int64_t grouped_sm100_most_tiles(const GroupedShape& s) {
   const int64_t few = (s.R < 40 * s.N ? s.R : 40 * s.N - 1) / 64, all = s.R / grouped_sm100_tile_rows(s);
   return (few > all ? few : all) + s.N;
@@ -450,6 +497,7 @@ cudaError_t launch_grouped_sm100(const GroupedShape& s, const GroupedPlan& p, Gr
   g.maps = static_cast<const CUtensorMap*>(p.maps);
   g.bias = static_cast<const __nv_bfloat16*>(bias);
   g.out = static_cast<__nv_bfloat16*>(out);
+  g.sums = p.sums;
   g.wait_ns = grouped_wait_ns(which == kGroupedFwd ? s.K : which == kGroupedDx ? s.O : s.R);
   g.shape.N = static_cast<int>(N);
   int64_t tiles;      // at most
@@ -494,7 +542,7 @@ cudaError_t launch_grouped_sm100(const GroupedShape& s, const GroupedPlan& p, Gr
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              static_cast<int>(kSmemLimit));
   if (e != cudaSuccess) return e;
-  const int64_t pairs = num_sms / 2;
+  const int64_t pairs = std::min(num_sms / 2, kSummingPairs);
   count_launch();
   return launch_dependent(kernel, dim3(static_cast<unsigned>(2 * (tiles < pairs ? tiles : pairs))),
                           dim3(kThreads), smem, stream, mapA, rows, mapOut, g);

@@ -10,8 +10,12 @@ namespace {
 
 struct Tile {
   int t;           // -1: no more
-  int e, m0, row0, rows, n, n0, kb;
+  int e, m0, row0, rows, n, n0;
+  int kb;          // steps, 64 deep
+  int k0;          // bf16: first step of this piece of the sum, and what it is joined with
+  int part;        //       (kAddSum, kKeepSum)
 };
+enum : int { kAddSum = 1, kKeepSum = 2 };
 
 // What the tile decoder needs.  off and prefix are read by ordinary loads: the plan writes
 // prefix while the product's CTAs may be on the GPU already, which rules out the read-only
