@@ -371,10 +371,14 @@ swl_status switch_layer_norm_residual_backward(int64_t T, int64_t d, int dtype, 
  * rounded to nearest, so a step that would move it by less than half a spacing (3 to 6% of
  * it; 2^-10 of the scale at least) leaves it: beta1 = 0.9 moves by a tenth of g - m, a
  * larger beta1 leaves more of a changed gradient out.  sqrt(v) is rounded stochastically
- * to one of the two e4m3 codes next to it with bits drawn from (element, t, seed), so the
- * same call gives the same result; a non-zero sqrt(v) keeps at least the smallest code,
- * 2^-9 of the scale (below it, it is held as that, whatever its gradients do).  A block
- * whose largest magnitude is under 2^-100 is held as zeros.  All-zero bytes and scales
+ * to three mantissa bits with bits drawn from (element, t, seed), so the same call gives
+ * the same result; a non-zero sqrt(v) keeps at least the smallest code, 2^-9.  From 2^-6 of
+ * the scaled value down (1/28672 of the block's largest root) e4m3 has fewer bits and the
+ * result is then rounded to nearest: there a root need not follow its gradients.  A faded
+ * gradient's stays (from 4 codes down for good), and one of the smallest code stands for
+ * gradients of up to 30 times it (beta2 = 0.999).  Elements whose gradients are that far
+ * apart take 32-bit states, or tensors of their own.  A block whose largest magnitude is
+ * under 2^-100 is held as zeros.  All-zero bytes and scales
  * are the zero state.  The step itself uses the unrounded m and v.
  * A gradient that is not finite makes its element's states and weight not finite
  * (8-bit states: the states of its whole block).

@@ -17,14 +17,15 @@
 // to nearest (its moving average renews a tenth of it per step with beta1 = 0.9, more than
 // half a spacing; with a larger beta1 less).  v is held by its root: r = sqrt(v) has half
 // the exponent range, so e4m3's 2^-9..448 spans 35 binary orders of v.  The root is rounded
-// stochastically to the codes next to it (three mantissa bits; from 2^-6 of the scaled
-// value down, where e4m3 has one spacing, multiples of 2^-9) with 16 random bits per
-// element: with b2 near 1 a step changes r by far less than half a spacing, and rounding
-// to nearest would never let v move.  The bits come from a counter (element pair, step,
-// seed) through two multiply-xorshift rounds, so a step can be repeated exactly.  A
-// non-zero r keeps at least the smallest code, so no element's denominator falls to eps
-// alone; a block whose largest magnitude is under 2^-100 is held as zeros.  The step itself
-// uses the unrounded m and v.
+// stochastically to three mantissa bits with 16 random bits per element: with b2 near 1 a
+// step changes r by far less than half a spacing, and rounding to nearest would never let
+// v move.  From 2^-6 down (1/28672 of the block's largest root, 24 of the 35 orders above
+// it) e4m3 has one spacing, 2^-9, and the conversion rounds to that, to nearest: there a
+// root may stand still, which the interface says.  The bits come from a counter (element
+// pair, step, seed) through two multiply-xorshift rounds, so a step can be repeated
+// exactly.  A non-zero r keeps at least the smallest code, so no element's denominator
+// falls to eps alone; a block whose largest magnitude is under 2^-100 is held as zeros.
+// The step itself uses the unrounded m and v.
 //
 // Bound: HBM.  Per element 12 bytes of fp32 weight and gradient (bf16: 6, with a
 // master 12) and 16 bytes of fp32 states or 4.06 of 8-bit ones.  One warp takes one
@@ -56,8 +57,6 @@ constexpr int kAdamBlock = SWL_ADAMW_BLOCK;         // elements that share a sca
 constexpr int kChunkBlocks = kAdamWarps;            // blocks a CTA takes at a time
 constexpr int kTableMax = 160;                      // tensors per launch (parameter space)
 constexpr float kLeast = 7.888609052210118e-31f;    // 2^-100
-constexpr float kSubnormal = 0.015625f;             // 2^-6: e4m3 below it has one spacing,
-constexpr float kSmallest = 0.001953125f;           // 2^-9
 
 struct AdamwEntry {
   void* p;
@@ -135,19 +134,6 @@ __device__ __forceinline__ unsigned mix(unsigned x) {
   x = (x ^ (x >> 16)) * 0x6A09E667u;
   x = (x ^ (x >> 15)) * 0xBB67AE85u;
   return x ^ (x >> 16);
-}
-
-// The scaled root q as one of the two codes next to it, the upper one with the probability
-// of what is cut: `bits` are 16 random bits over the cut ones.  Under 2^-6 the codes are
-// 2^-9 apart, as numbers of three mantissa bits are from 2^-6 to 2^-5: rounded there and
-// moved back.
-__device__ __forceinline__ float root_code(float q, unsigned bits) {
-  const bool low = q < kSubnormal;
-  float x = q;
-  if (low) x = __fadd_rn(x, kSubnormal);
-  x = __uint_as_float((__float_as_uint(x) + (bits << 4) + 8u) & 0xfff00000u);
-  if (low) x = fmaxf(__fsub_rn(x, kSubnormal), kSmallest);
-  return q <= 0.f ? 0.f : x;
 }
 
 // Four consecutive elements as they lie in memory: float4 (fp32), uint2 (bf16) or
@@ -337,7 +323,10 @@ struct Block {
           const unsigned u = mix(static_cast<unsigned>((i0 + j) >> 1) + R.key);
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            x[j + k] = root_code(__fmul_rn(fv[h][j + k], ir), k ? u >> 16 : u & 0xffffu);
+            const float q = __fmul_rn(fv[h][j + k], ir);
+            const unsigned t = (__float_as_uint(q) + ((k ? u >> 16 : u & 0xffffu) << 4) + 8u) &
+                               0xfff00000u;
+            x[j + k] = q <= 0.f ? 0.f : max_nan(__uint_as_float(t), 0.001953125f);
             fm[h][j + k] = __fmul_rn(fm[h][j + k], im);
           }
         }
@@ -356,8 +345,7 @@ struct Block {
 // before the current one is worked on, so that the loads overlap the arithmetic
 // (a warp issues about 75 instructions per element of an 8-bit state; measured on
 // 202 M bf16 parameters with masters and 8-bit states: 722 -> 635 us in a run of calls,
-// 574 us alone, 5.6 TB/s; 566 with roots rounded to three mantissa bits everywhere, which
-// never moves one of a few 2^-9).
+// 566 us alone, 5.7 TB/s).
 template <typename P, bool kMaster, bool kEight>
 __device__ __forceinline__ void step_tensor(const AdamwEntry& e, long long b, long long stride,
                                             const Rates& R) {
