@@ -19,7 +19,7 @@
 // the exponent range, so e4m3's 2^-9..448 spans 35 binary orders of v.  The root is rounded
 // stochastically to three mantissa bits with 16 random bits per element: with b2 near 1 a
 // step changes r by far less than half a spacing, and rounding to nearest would never let
-// v move.  From 2^-6 down (1/28672 of the block's largest root, 24 of the 35 orders above
+// v move.  From 2^-6 down (1/28672 of the block's largest root, 30 of the 35 orders above
 // it) e4m3 has one spacing, 2^-9, and the conversion rounds to that, to nearest: there a
 // root may stand still, which the interface says.  The bits come from a counter (element
 // pair, step, seed) through two multiply-xorshift rounds, so a step can be repeated
