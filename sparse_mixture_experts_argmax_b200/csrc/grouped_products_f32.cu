@@ -27,13 +27,14 @@
 // products of a 64-deep step take 2048 cycles and its 12288 elements about 600 issue
 // cycles of splitting, for fewer rows the loads bound it.
 //
-// Measured: 4095 rows over 60 groups, 765 -> 1021 (no row aligned): 128 us, bytes 33 us;
-// 16384 rows over 8 groups, 1024 -> 2048: 513 us, 134 TFLOP/s of fp32 products (fp32 FMA
+// Measured: 4095 rows over 60 groups, 765 -> 1021 (no row aligned): 130 us, bytes 33 us;
+// 16384 rows over 8 groups, 1024 -> 2048: 516 us, 133 TFLOP/s of fp32 products (fp32 FMA
 // tiles took 367 us for the first).  A step takes about 2.2 us, the converters' loads,
 // splits and stores following one another in 8 warps; what is left of it is there.
 //
 // Roles of a CTA's 20 warps: 0 MMA issuer (first CTA only), 1 TMEM, 2 tile decoder, 3
-// relay between the converters and the first CTA, 4-11 sums and stores (two warps per lane quarter), 12-19 converters.
+// relay between the converters and the first CTA, 4-11 sums and stores (two warps per
+// lane quarter), 12-19 converters.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

@@ -35,8 +35,8 @@
 //
 // Bound: tensor cores for groups of many rows (32768 x 2048 by 8 groups of 5120 x 2048:
 // 490 us, 1.40 PFLOP/s, 0.86 of the burst peak), W's bytes for few (16384 rows over 128
-// groups, 1024 -> 4096: y 207 us and dx 193 us where the bytes take 189 us), dW's stores
-// (the same sizes: 258 us; a plain fill of 1.07 GB takes 275 us).
+// groups, 1024 -> 4096: y 208 us and dx 194 us where the bytes take 189 us), dW's stores
+// (the same sizes: 259 us; a plain fill of 1.07 GB takes 275 us).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

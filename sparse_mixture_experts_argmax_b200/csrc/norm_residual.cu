@@ -32,7 +32,7 @@
 // result every time.
 //
 // Measured at 32768 x 2048 bf16, RMS norms on both sides, gate and scale: forward 110 us
-// (floor 82 us), backward 242 us (floor 123 us); one row of 1024: 2.7 us in a graph.  The
+// (floor 82 us), backward 243 us (floor 123 us); one row of 1024: 2.7 us in a graph.  The
 // backward pass issues 60 instructions per element on 16 warps per SM (the column sums
 // take their registers) and moves 24 KB of fp32 parameters per row through L1.
 #include <cuda_bf16.h>
