@@ -302,7 +302,9 @@ swl_status switch_layer_grouped_matmul_backward(int64_t R, int64_t K, int64_t O,
  * would take that factor out, and the router's gradient through the layer with it, so
  * w_post goes with ungated rows and gate.  y NULL: only h = n(x); then r is NULL.  h NULL (and w_pre
  * NULL): no second norm.  Sums and statistics are fp32; r and h are each rounded
- * once (h is taken from the unrounded r).
+ * once (h is taken from the unrounded r).  A row whose sums pass fp32's range (values of
+ * about 1e19 and more, a mask's lowest value among them) has no norm: its h and its
+ * gradients are 0 or not finite, and the parameters' gradients may not be finite either.
  *   x, y, r, h      [T, d] of dtype; r and h may be x or y themselves (in place), but
  *                   not overlap them otherwise, nor each other
  *   gate [T], w_*, b_*, scale [d]   fp32
@@ -381,7 +383,9 @@ swl_status switch_layer_norm_residual_backward(int64_t T, int64_t d, int dtype, 
  * under 2^-100 is held as zeros.  All-zero bytes and scales
  * are the zero state.  The step itself uses the unrounded m and v.
  * A gradient that is not finite makes its element's states and weight not finite
- * (8-bit states: the states of its whole block).
+ * (8-bit states: the states of its whole block).  A square that passes fp32's range (a
+ * gradient of 2^64 and more) makes v infinite: with 32-bit states its element then only
+ * decays, with 8-bit ones its block's states are not finite.
  *   tensors, count  host array; tensors of different types may be mixed; n = 0 is
  *                   allowed (pointers may then be NULL)
  *   step            DEVICE int32 [2]: the steps made so far, and a word that is
